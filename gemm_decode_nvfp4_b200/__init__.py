@@ -25,6 +25,8 @@ __all__ = [
     "mx_quantize", "mx_quantize_new", "mx_gemv", "gemv_grouped", "mx_to_nvfp4",
     "GIVEN_AMAX", "w4a4_prepare_weights", "w4a4_quantize_x", "w4a4_gemm", "w4a4_linear",
     "w4a4_workspace_size", "AMAX_FLOATS",
+    "fp8_rmsnorm", "fp8_quantize", "fp8_quantize_new", "fp8_quantize_weights", "fp8_quantize_weights_new",
+    "fp8_gemm", "fp8_gemm_grouped", "fp8_linear",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +34,7 @@ LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "nvfp4.h")
 MX_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxfp4.h")
 W4A4_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "nvfp4_w4a4.h")
+FP8_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp8.h")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python gemm_decode_nvfp4_b200/build.py`")
@@ -64,13 +67,19 @@ lib.nvfp4_w4a4_gemm.argtypes = [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i
 lib.nvfp4_w4a4_linear.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _sz, ctypes.c_uint32, _p]
 lib.mxfp4_gemv.argtypes = [_p, _p, _p, _p, _i64, _i64, _p]
 lib.mxfp4_gemv_ex.argtypes = [_p, _p, _p, _p, _i64, _i64, ctypes.c_uint32, _p]
+lib.fp8_rmsnorm.argtypes = [_p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _i64, ctypes.c_float, _p]
+lib.fp8_quantize.argtypes = [_p, _i64, _i64, _i64, _p, _p, ctypes.c_uint32, _p]
+lib.fp8_quantize_weights.argtypes = [_p, _i64, _i64, _i64, _p, _p, _p]
+lib.fp8_gemm.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, ctypes.c_uint32, _p]
+lib.fp8_gemm_grouped.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, ctypes.c_uint32, _p]
 lib.nvfp4_gemm_workspace_size.restype = _sz
 lib.nvfp4_check_device_errors.argtypes = []
 for _f in (lib.nvfp4_amax, lib.nvfp4_quantize, lib.nvfp4_quantize_mse, lib.nvfp4_gemv, lib.nvfp4_gemm, lib.nvfp4_gemv_ex, lib.nvfp4_gemm_ex,
            lib.nvfp4_gemm_noalloc, lib.nvfp4_check_device_errors, lib.mxfp4_quantize, lib.mxfp4_gemv,
            lib.mxfp4_gemv_ex, lib.nvfp4_gemv_grouped, lib.mxfp4_to_nvfp4_scales,
            lib.nvfp4_w4a4_prepare_weights, lib.nvfp4_w4a4_quantize_x, lib.nvfp4_w4a4_gemm,
-           lib.nvfp4_w4a4_linear):
+           lib.nvfp4_w4a4_linear, lib.fp8_rmsnorm, lib.fp8_quantize, lib.fp8_quantize_weights, lib.fp8_gemm,
+           lib.fp8_gemm_grouped):
     _f.restype = ctypes.c_int
 
 
@@ -97,11 +106,11 @@ def version() -> int:
 
 
 def declared_symbols() -> list[str]:
-    """Names of the entry points include/nvfp4.h, mxfp4.h and nvfp4_w4a4.h declare."""
+    """Names of the entry points include/nvfp4.h, mxfp4.h, nvfp4_w4a4.h and fp8.h declare."""
     names = []
-    for path in (HEADER_PATH, MX_HEADER_PATH, W4A4_HEADER_PATH):
+    for path in (HEADER_PATH, MX_HEADER_PATH, W4A4_HEADER_PATH, FP8_HEADER_PATH):
         with open(path) as f:
-            names += re.findall(r"NVFP4_API\s+[\w\s\*]+?\b((?:nvfp4|mxfp4)_\w+)\s*\(", f.read())
+            names += re.findall(r"NVFP4_API\s+[\w\s\*]+?\b((?:nvfp4|mxfp4|fp8)_\w+)\s*\(", f.read())
     return names
 
 
@@ -499,3 +508,148 @@ def w4a4_linear(X: torch.Tensor, q: torch.Tensor, s_mma: torch.Tensor, g: torch.
     dev = _device(X, x_amax, q, s_mma, g, Y, workspace)
     _call("nvfp4_w4a4_linear", dev, _ptr(X), X.stride(0), _ptr(x_amax), _ptr(q), _ptr(s_mma), _ptr(g), _ptr(Y),
           Y.stride(0), M, N, K, _ptr(workspace), workspace.numel(), flags, _stream(stream, dev))
+
+
+# ------------------------------------------------------------------------ FP8
+# 8-bit linear layer (include/fp8.h): E4M3 values with one fp32 scale per row
+# and 128 columns (activations) or per 128 x 128 block (weights).
+
+FLAG_FP8_GATED = 2
+_F8 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _ld(t: torch.Tensor | None) -> int:
+    """Leading dimension of a 2-D tensor; of a single row, whose stride says nothing, its length."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _need_fp8(q: torch.Tensor, s: torch.Tensor, what: str, shape: tuple, scale_shape: tuple):
+    """q float8_e4m3fn of `shape` and its scales s float32 of `scale_shape`, both contiguous."""
+    _need(q, _F8, what)
+    _need(s, torch.float32, f"{what}'s scales")
+    if tuple(q.shape) != shape or tuple(s.shape) != scale_shape or not q.is_contiguous() or not s.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {list(shape)} with scales {list(scale_shape)}, got "
+                         f"{tuple(q.shape)} and {tuple(s.shape)}")
+
+
+def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                q: torch.Tensor | None = None, s: torch.Tensor | None = None, stream=None) -> None:
+    """RMS norm of BF16 x [M, K] (+ residual) times weight [K].  With a residual,
+    residual_out (default: residual itself, in place) receives bf16(x + residual),
+    which is what is normed.  Outputs, at least one: y BF16 [M, K], and
+    q float8_e4m3fn [M, K] with s float32 [M, ceil(K/128)]."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(weight, torch.bfloat16, "weight", 1)
+    M, K = x.shape
+    if weight.shape[0] != K:
+        raise ValueError(f"weight must hold K={K} elements, got {weight.shape[0]}")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
+        if t is not None:
+            _need(t, torch.bfloat16, what, 2)
+            if t.shape != x.shape:
+                raise ValueError(f"{what} must be {tuple(x.shape)}, got {tuple(t.shape)}")
+    if (q is None) != (s is None):
+        raise ValueError("q and s go together")
+    if q is not None:
+        _need_fp8(q, s, "q", (M, K), (M, _blocks(K)))
+    dev = _device(x, weight, residual, residual_out, y, q, s)
+    _call("fp8_rmsnorm", dev, _ptr(x), _ld(x), _ptr(weight), _ptr(residual), _ld(residual), _ptr(residual_out),
+          _ld(residual_out), _ptr(y), _ld(y), _ptr(q), _ptr(s), M, K, float(eps), _stream(stream, dev))
+
+
+def fp8_quantize(X: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gated: bool = False, stream=None) -> None:
+    """BF16 activations X [M, K] into q float8_e4m3fn [M, K] and s float32 [M, ceil(K/128)].
+    gated: X is [M, 2K], gate then up columns, and silu(gate) * up is quantized."""
+    _need(X, torch.bfloat16, "X", 2)
+    M, cols = X.shape
+    if gated and cols % 2:
+        raise ValueError(f"a gated X has an even number of columns, got {cols}")
+    K = cols // 2 if gated else cols
+    _need_fp8(q, s, "q", (M, K), (M, _blocks(K)))
+    dev = _device(X, q, s)
+    _call("fp8_quantize", dev, _ptr(X), _ld(X), M, K, _ptr(q), _ptr(s), FLAG_FP8_GATED if gated else 0,
+          _stream(stream, dev))
+
+
+def fp8_quantize_weights(W: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """BF16 weights W [N, K] into q float8_e4m3fn [N, K] and s float32 [ceil(N/128), ceil(K/128)]."""
+    _need(W, torch.bfloat16, "W", 2)
+    N, K = W.shape
+    _need_fp8(q, s, "q", (N, K), (_blocks(N), _blocks(K)))
+    dev = _device(W, q, s)
+    _call("fp8_quantize_weights", dev, _ptr(W), _ld(W), N, K, _ptr(q), _ptr(s), _stream(stream, dev))
+
+
+def fp8_gemm(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, Y: torch.Tensor, stream=None,
+             static_weights: bool = False) -> None:
+    """Y [M, N] = bf16((x * sx) . (w * sw)^T): activations x [M, K], sx [M, ceil(K/128)]
+    (fp8_quantize, fp8_rmsnorm), weights w [N, K], sw [ceil(N/128), ceil(K/128)]
+    (fp8_quantize_weights).  static_weights: w is not written by work still
+    running on the stream (NVFP4_FLAG_STATIC_WEIGHTS)."""
+    _need(x, _F8, "x", 2)
+    _need(w, _F8, "w", 2)
+    _need(Y, torch.bfloat16, "Y", 2)
+    (M, K), N = x.shape, w.shape[0]
+    _need_fp8(x, sx, "x", (M, K), (M, _blocks(K)))
+    _need_fp8(w, sw, "w", (N, K), (_blocks(N), _blocks(K)))
+    if Y.shape != (M, N):
+        raise ValueError(f"Y must be {(M, N)}, got {tuple(Y.shape)}")
+    dev = _device(x, sx, w, sw, Y)
+    _call("fp8_gemm", dev, _ptr(x), _ptr(sx), _ptr(w), _ptr(sw), _ptr(Y), _ld(Y), M, N, K,
+          FLAG_STATIC_WEIGHTS if static_weights else 0, _stream(stream, dev))
+
+
+def fp8_gemm_grouped(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, offsets: torch.Tensor,
+                     Y: torch.Tensor, stream=None, static_weights: bool = False) -> None:
+    """fp8_gemm by expert: rows offsets[e] .. offsets[e+1]-1 of x [T, K] and Y [T, N]
+    belong to expert e of w [E, N, K], sw [E, ceil(N/128), ceil(K/128)].  offsets:
+    int32 [E + 1] on the device, not decreasing.  Rows of Y outside
+    offsets[0] .. offsets[E]-1 keep what they hold."""
+    _need(x, _F8, "x", 2)
+    _need(w, _F8, "w", 3)
+    _need(offsets, torch.int32, "offsets", 1)
+    _need(Y, torch.bfloat16, "Y", 2)
+    (T, K), (E, N) = x.shape, w.shape[:2]
+    _need_fp8(x, sx, "x", (T, K), (T, _blocks(K)))
+    _need_fp8(w, sw, "w", (E, N, K), (E, _blocks(N), _blocks(K)))
+    if Y.shape != (T, N) or offsets.shape[0] != E + 1:
+        raise ValueError(f"Y must be {(T, N)} and offsets hold {E + 1}, got {tuple(Y.shape)} and {offsets.shape[0]}")
+    dev = _device(x, sx, w, sw, offsets, Y)
+    _call("fp8_gemm_grouped", dev, _ptr(x), _ptr(sx), _ptr(w), _ptr(sw), _ptr(offsets), _ptr(Y), _ld(Y), T, E, N,
+          K, FLAG_STATIC_WEIGHTS if static_weights else 0, _stream(stream, dev))
+
+
+def fp8_quantize_new(X: torch.Tensor, gated: bool = False, stream=None):
+    """Allocate q, s on X's device and quantize activations into them."""
+    M, K = X.shape[0], X.shape[1] // 2 if gated else X.shape[1]
+    q = torch.empty((M, K), dtype=_F8, device=X.device)
+    s = torch.empty((M, _blocks(K)), dtype=torch.float32, device=X.device)
+    fp8_quantize(X, q, s, gated=gated, stream=stream)
+    return q, s
+
+
+def fp8_quantize_weights_new(W: torch.Tensor, stream=None):
+    """Allocate q, s on W's device and quantize weights into them."""
+    N, K = W.shape
+    q = torch.empty((N, K), dtype=_F8, device=W.device)
+    s = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
+    fp8_quantize_weights(W, q, s, stream=stream)
+    return q, s
+
+
+def fp8_linear(X: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, stream=None) -> torch.Tensor:
+    """Quantize BF16 X [M, K] and multiply by 8-bit weights: allocates and returns Y [M, N]."""
+    X2 = X if X.dim() == 2 else X.reshape(1, -1)
+    q, s = fp8_quantize_new(X2, stream=stream)
+    Y = torch.empty((X2.shape[0], w.shape[0]), dtype=torch.bfloat16, device=X.device)
+    fp8_gemm(q, s, w, sw, Y, stream=stream)
+    return Y if X.dim() == 2 else Y.reshape(-1)

@@ -90,6 +90,8 @@ nvfp4_status nvfp4::report_error(nvfp4_status st, const char* fmt, ...) {
 
 nvfp4_status nvfp4::report_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
+nvfp4_status nvfp4::require_device(int* sms) { return check_device(sms); }
+
 extern "C" {
 
 int nvfp4_version(void) { return 100; }
@@ -545,6 +547,9 @@ nvfp4_status nvfp4_check_device_errors(void) {
   cudaError_t e = nvfp4::read_and_clear_gemm_timeouts(&n);
   if (e == cudaSuccess) e = nvfp4::read_and_clear_w4a4_timeouts(&w);
   n += w;
+  unsigned int f8 = 0, bad_offsets = 0;
+  if (e == cudaSuccess) e = nvfp4::read_and_clear_fp8_errors(&f8, &bad_offsets);
+  n += f8;
   if (e == cudaSuccess) e = nvfp4::read_and_clear_small_timeouts(&k);
   if (e == cudaSuccess) e = nvfp4::read_and_clear_gemv_timeouts(&v);
   unsigned int bad = 0, window = 0;
@@ -554,6 +559,8 @@ nvfp4_status nvfp4_check_device_errors(void) {
   if (n || k || v)
     return fail(NVFP4_ERR_TIMEOUT, "%u GEMM, %u small-M GEMM and %u GEMV CTA(s) gave up on a pipeline wait", n, k, v);
   if (bad) return fail(NVFP4_ERR_INVALID_ARG, "%u grouped GEMV problem(s) had an out-of-range expert or token id", bad);
+  if (bad_offsets)
+    return fail(NVFP4_ERR_INVALID_ARG, "%u grouped fp8 GEMM call(s) had offsets that decrease or leave 0..T", bad_offsets);
   if (window)
     return fail(NVFP4_ERR_INVALID_ARG, "%u MXFP4 block(s) could not be restated as NVFP4 scales (more than 17 binades "
                 "below the largest, or NaN)", window);

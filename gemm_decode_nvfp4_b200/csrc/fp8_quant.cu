@@ -1,0 +1,363 @@
+// fp8_quant.cu -- the kernels that write E4M3 values with one fp32 scale per
+// 128: the RMS norm with the residual's addition, the activation quantizer
+// (plain, or of silu(gate) * up) and the weight quantizer (include/fp8.h).
+//
+// One rule everywhere, over a block of 128 columns of one row (activations) or
+// of 128 rows (weights):
+//   s = max(max|v| / 448, 2^-126),  q = E4M3_rne_satfinite(v * (1 / s))
+// with IEEE fp32 divisions.  The lower limit keeps 1 / s finite.
+// fmaxf drops NaN, so a NaN element stays a NaN code of its own and leaves the
+// rest of its block alone; an infinity makes its block's scale infinite.
+//
+// All three stream HBM once.  A thread owns 16-byte vectors (8 columns) that
+// are consecutive across lanes, so a block of 128 columns is 16 neighbouring
+// lanes and its maximum takes four shuffles; K is a multiple of 16, so no
+// vector straddles the end of a row.
+#include "nvfp4_device.cuh"
+#include "nvfp4_kernels.h"
+#include "tc_host.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16lo_to_float(w[i]);
+    f[2 * i + 1] = bf16hi_to_float(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ float absmax(const float (&f)[8]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
+  return a;
+}
+
+// maximum over the 16 lanes that share a block of 128 columns
+__device__ __forceinline__ float max16(float a) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  return a;
+}
+
+__device__ __forceinline__ float scale_of(float amax) { return fmaxf(__fdiv_rn(amax, 448.0f), kScaleMin); }
+
+// (lo, hi) -> two E4M3 bytes, lo in the low one
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t out;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
+  return out;
+}
+
+__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float r) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = e4m3x2(__fmul_rn(f[2 * i], r), __fmul_rn(f[2 * i + 1], r));
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* w;
+  const uint16_t* res;  // null: none
+  uint16_t* res_out;
+  uint16_t* y;  // null: none
+  uint8_t* q;   // null: none
+  float* s;
+  int64_t ldx, ldr, ldro, ldy;
+  int64_t M;
+  int K, kb;
+  float eps;
+};
+
+// x (+ residual) of one vector: what the norm is taken of.  The sum is used as
+// its BF16 value, the one that the residual stream carries on.
+__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c, float (&f)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(a.x + row * a.ldx + c), f);
+  if (a.res) {
+    float r[8];
+    unpack8(*reinterpret_cast<const uint4*>(a.res + row * a.ldr + c), r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(f[i], r[i]);
+    unpack8(pack8(f), f);
+  }
+}
+
+__device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int c, bool in, float (&f)[8], uint4 wv,
+                                         float rstd) {
+  float w[8];
+  unpack8(wv, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], rstd), w[i]);
+  if (a.y && in) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = pack8(f);
+  if (a.q) {
+    const float s = scale_of(max16(absmax(f)));
+    if (in) {
+      *reinterpret_cast<uint2*>(a.q + row * a.K + c) = quantize8(f, __frcp_rn(s));
+      if ((c & 127) == 0) a.s[row * a.kb + (c >> 7)] = s;
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// RMS norm: `threads` (a multiple of 32) threads per row, VPT vectors each, the
+// row kept in registers between the sum of squares and the output.  threads
+// == 32 takes 4 rows per CTA and needs no barrier.
+template <int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int threads) {
+  __shared__ float red[32];
+  const int t = threadIdx.x % threads;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / threads) + threadIdx.x / threads;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= a.M) return;  // whole warps: one row's threads stay together
+  float f[VPT][8];
+  uint4 wv[VPT];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (t + i * threads) * 8;
+    if (c < a.K) {
+      load_h(a, row, c, f[i]);
+      wv[i] = __ldg(reinterpret_cast<const uint4*>(a.w + c));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+      wv[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
+  if (a.res_out) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (t + i * threads) * 8;
+      if (c < a.K) *reinterpret_cast<uint4*>(a.res_out + row * a.ldro + c) = pack8(f[i]);
+    }
+  }
+  sum = warp_sum(sum);
+  if (threads > 32) {
+    if ((t & 31) == 0) red[t >> 5] = sum;
+    __syncthreads();
+    sum = warp_sum((t & 31) < (threads >> 5) ? red[t & 31] : 0.0f);
+  }
+  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.K), a.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (t + i * threads) * 8;
+    norm_out(a, row, c, c < a.K, f[i], wv[i], rstd);
+  }
+}
+
+// Rows too long for registers: 1024 threads walk the row twice, the second time
+// (out of L2) over residual_out where there is one.
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
+  __shared__ float red[32];
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float sum = 0.0f;
+  for (int c = t * 8; c < a.K; c += 8192) {
+    float f[8];
+    load_h(a, row, c, f);
+    if (a.res_out) *reinterpret_cast<uint4*>(a.res_out + row * a.ldro + c) = pack8(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+  }
+  sum = warp_sum(sum);
+  if ((t & 31) == 0) red[t >> 5] = sum;
+  __syncthreads();
+  sum = warp_sum(red[t & 31]);
+  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.K), a.eps));
+  NormArgs b = a;
+  if (a.res_out) {  // written above by this same thread
+    b.x = a.res_out;
+    b.ldx = a.ldro;
+    b.res = nullptr;
+  }
+  for (int c0 = 0; c0 < a.K; c0 += 8192) {  // whole warps: the block maxima shuffle
+    const int c = c0 + t * 8;
+    const bool in = c < a.K;
+    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    if (in) {
+      load_h(b, row, c, f);
+      wv = __ldg(reinterpret_cast<const uint4*>(a.w + c));
+    }
+    norm_out(a, row, c, in, f, wv, rstd);
+  }
+}
+
+struct QuantArgs {
+  const uint16_t* x;
+  uint8_t* q;
+  float* s;
+  int64_t ldx;
+  uint32_t blocks;  // M * kb
+  int K, kb;
+};
+
+// silu(g) * u in fp32
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fmul_rn(__fdividef(g, 1.0f + __expf(-g)), u);
+}
+
+template <bool GATED>
+__device__ __forceinline__ void quant_load(const QuantArgs& a, uint32_t blk, int lane16, uint4& v, uint4& u, bool& in) {
+  const uint32_t row = blk / (uint32_t)a.kb;
+  const int c = (int)(blk - row * (uint32_t)a.kb) * 128 + lane16 * 8;
+  in = blk < a.blocks && c < a.K;
+  v = u = make_uint4(0, 0, 0, 0);
+  if (in) {
+    const uint16_t* p = a.x + (int64_t)row * a.ldx + c;
+    v = ld_stream_v4(p);
+    if (GATED) u = ld_stream_v4(p + a.K);
+  }
+}
+
+template <bool GATED>
+__device__ __forceinline__ void quant_store(const QuantArgs& a, uint32_t blk, int lane16, uint4 v, uint4 u, bool in) {
+  float f[8];
+  unpack8(v, f);
+  if (GATED) {
+    float uf[8];
+    unpack8(u, uf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = silu_mul(f[i], uf[i]);
+  }
+  const float s = scale_of(max16(absmax(f)));
+  if (in) {
+    const uint32_t row = blk / (uint32_t)a.kb;
+    const int c = (int)(blk - row * (uint32_t)a.kb) * 128 + lane16 * 8;
+    *reinterpret_cast<uint2*>(a.q + (int64_t)row * a.K + c) = quantize8(f, __frcp_rn(s));
+    if (lane16 == 0) a.s[blk] = s;
+  }
+}
+
+// Activation quantizer: 16 lanes per block of 128 columns.
+template <bool GATED>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane16 = threadIdx.x & 15;
+  const uint64_t stride = (uint64_t)gridDim.x * 16;
+  // (whole warps stay in the loop: both halves of a warp take part in the shuffles)
+  for (uint64_t b = (uint64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; b < a.blocks; b += stride) {
+    const uint32_t blk = (uint32_t)b + ((threadIdx.x >> 4) & 1);
+    uint4 v, u;
+    bool in;
+    quant_load<GATED>(a, blk, lane16, v, u, in);
+    quant_store<GATED>(a, blk, lane16, v, u, in);
+  }
+}
+
+// Weight quantizer: one CTA of 256 threads per 128 x 128 block, held in
+// registers between the maximum and the codes.
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const uint16_t* __restrict__ w, int64_t ldw, int64_t N,
+                                                              int K, int kb, uint8_t* __restrict__ q,
+                                                              float* __restrict__ s) {
+  __shared__ float red[8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t nb = blockIdx.x / kb;
+  const int b = (int)(blockIdx.x - nb * kb);
+  const int c = b * 128 + (threadIdx.x & 15) * 8;
+  const int64_t row0 = nb * 128 + (threadIdx.x >> 4);
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = row0 + 16 * i;
+    v[i] = n < N && c < K ? ld_stream_v4(w + n * ldw + c) : make_uint4(0, 0, 0, 0);
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    unpack8(v[i], f);
+    m = fmaxf(m, absmax(f));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+  const float sc = scale_of(m), r = __frcp_rn(sc);
+  if (threadIdx.x == 0) s[blockIdx.x] = sc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = row0 + 16 * i;
+    if (n < N && c < K) {
+      float f[8];
+      unpack8(v[i], f);
+      *reinterpret_cast<uint2*>(q + n * K + c) = quantize8(f, r);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* weight, const uint16_t* residual,
+                               int64_t ldr, uint16_t* residual_out, int64_t ldro, uint16_t* y, int64_t ldy, uint8_t* q,
+                               float* s, int64_t M, int64_t K, float eps, cudaStream_t stream) {
+  NormArgs a{x, weight, residual, residual_out, y, q, s, ldx, ldr, ldro, ldy, M, (int)K, (int)((K + 127) / 128), eps};
+  const int64_t vecs = K / 8;
+  if (vecs > 1024 * 4) {
+    void* args[] = {&a};
+    return tc::launch_pdl((const void*)rmsnorm_long_kernel, dim3((unsigned)M), dim3(1024), 0, stream, args);
+  }
+  // one warp per row while four vectors a lane hold it, else up to four vectors a thread
+  int vpt = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4, threads = 32;
+  if (vecs > 128) {
+    vpt = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+    threads = (int)(((vecs + vpt - 1) / vpt + 31) / 32 * 32);
+  }
+  const int rows = threads == 32 ? 4 : 1;
+  void* args[] = {&a, &threads};
+  const void* fn = vpt == 1 ? (const void*)rmsnorm_kernel<1> : vpt == 2 ? (const void*)rmsnorm_kernel<2>
+                                                                       : (const void*)rmsnorm_kernel<4>;
+  return tc::launch_pdl(fn, dim3((unsigned)((M + rows - 1) / rows)), dim3(threads * rows), 0, stream, args);
+}
+
+cudaError_t launch_fp8_quantize(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, bool gated, uint8_t* q, float* s,
+                                int sms, cudaStream_t stream) {
+  const int64_t kb = (K + 127) / 128;
+  QuantArgs a{x, q, s, ldx, (uint32_t)(M * kb), (int)K, (int)kb};
+  const int64_t want = (M * kb + 15) / 16, most = (int64_t)sms * 8;
+  void* args[] = {&a};
+  return tc::launch_pdl(gated ? (const void*)quantize_rows_kernel<true> : (const void*)quantize_rows_kernel<false>,
+                        dim3((unsigned)(want < most ? want : most)), dim3(256), 0, stream, args);
+}
+
+cudaError_t launch_fp8_quantize_weights(const uint16_t* w, int64_t ldw, int64_t N, int64_t K, uint8_t* q, float* s,
+                                        cudaStream_t stream) {
+  int kb = (int)((K + 127) / 128), k = (int)K;
+  const int64_t blocks = (N + 127) / 128 * kb;
+  void* args[] = {&w, &ldw, &N, &k, &kb, &q, &s};
+  return tc::launch_pdl((const void*)quantize_blocks_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, args);
+}
+
+}  // namespace nvfp4

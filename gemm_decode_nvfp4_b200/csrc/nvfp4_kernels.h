@@ -105,6 +105,27 @@ cudaError_t read_and_clear_small_timeouts(unsigned int* count);
 nvfp4_status report_error(nvfp4_status st, const char* fmt, ...);
 nvfp4_status report_cuda_error(cudaError_t e, const char* what);
 
+// NVFP4_OK and the SM count if the current device is a B200-class part, else the
+// recorded error.
+nvfp4_status require_device(int* sms);
+
+// 8-bit linear layer (include/fp8.h).  fp8_quant.cu: the RMS norm with its
+// optional residual, BF16 and 8-bit outputs, the activation quantizer, the
+// weight quantizer.
+cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* weight, const uint16_t* residual,
+                               int64_t ldr, uint16_t* residual_out, int64_t ldro, uint16_t* y, int64_t ldy, uint8_t* q,
+                               float* s, int64_t M, int64_t K, float eps, cudaStream_t stream);
+cudaError_t launch_fp8_quantize(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, bool gated, uint8_t* q, float* s,
+                                int sms, cudaStream_t stream);
+cudaError_t launch_fp8_quantize_weights(const uint16_t* w, int64_t ldw, int64_t N, int64_t K, uint8_t* q, float* s,
+                                        cudaStream_t stream);
+// fp8_gemm.cu: the product; offsets null: dense (E == 1), else grouped by expert.
+cudaError_t launch_fp8_gemm(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, const int* offsets,
+                            uint16_t* Y, int64_t ldy, int64_t T, int64_t E, int64_t N, int64_t K, bool static_weights,
+                            int sms, cudaStream_t stream);
+// CTAs whose bounded wait gave up, and grouped calls with bad offsets, since the last read.
+cudaError_t read_and_clear_fp8_errors(unsigned int* timeouts, unsigned int* bad_offsets);
+
 // Largest K the GEMV accepts (x is staged in shared memory as fp32).
 constexpr int64_t kGemvMaxK = 49152;
 
