@@ -116,24 +116,33 @@ def declared_symbols() -> list[str]:
 
 def _device(*tensors) -> torch.device:
     """The one CUDA device all the given tensors (None skipped) live on."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors must all be on one CUDA device, got {sorted(str(d) for d in devs)}")
-    return devs.pop()
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                devs = sorted({str(u.device) for u in tensors if u is not None})
+                raise ValueError(f"tensors must all be on one CUDA device, got {devs}")
+    return dev
 
 
 def _stream(stream, dev: torch.device) -> int:
     """The raw stream handle for a call on `dev`: the given stream (which must
     belong to `dev`) or that device's current stream."""
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
-    return s.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
 
 
 def _call(fn: str, dev: torch.device, *args) -> None:
     """Call lib.<fn>(*args) with `dev` current (the library launches on the
     current device) and raise on a non-zero status."""
+    if torch.cuda.current_device() == dev.index:
+        _check(fn, getattr(lib, fn)(*args))
+        return
     with torch.cuda.device(dev):
         _check(fn, getattr(lib, fn)(*args))
 
@@ -529,9 +538,10 @@ def _ld(t: torch.Tensor | None) -> int:
 
 def _need_fp8(q: torch.Tensor, s: torch.Tensor, what: str, shape: tuple, scale_shape: tuple):
     """q float8_e4m3fn of `shape` and its scales s float32 of `scale_shape`, both contiguous."""
-    _need(q, _F8, what)
-    _need(s, torch.float32, f"{what}'s scales")
-    if tuple(q.shape) != shape or tuple(s.shape) != scale_shape or not q.is_contiguous() or not s.is_contiguous():
+    if not (q.dtype is _F8 and q.is_cuda and s.dtype is torch.float32 and s.is_cuda):
+        _need(q, _F8, what)
+        _need(s, torch.float32, f"{what}'s scales")
+    if q.shape != shape or s.shape != scale_shape or not q.is_contiguous() or not s.is_contiguous():
         raise ValueError(f"{what} must be contiguous {list(shape)} with scales {list(scale_shape)}, got "
                          f"{tuple(q.shape)} and {tuple(s.shape)}")
 

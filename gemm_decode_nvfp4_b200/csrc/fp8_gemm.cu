@@ -26,6 +26,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -39,12 +41,13 @@ __device__ unsigned int g_fp8_bad_offsets = 0;
 
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr long long kWaitClocks = 4000000000ll;  // about 2 s
+constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kRows = 128;        // MMA M
 constexpr int kBlockK = 128;      // k per stage, one scale block, one swizzled row
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 4;
-constexpr int kScaleSlots = 12;   // >= stages + accumulator buffers
+constexpr int kScaleSlots = 16;
 constexpr int kGroupTiles = 16;   // token tiles that share a weight tile in the tile order
 
 struct Args {
@@ -60,13 +63,20 @@ struct Args {
 struct Bars {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t sfull[kScaleSlots];
+  uint64_t sfull[kScaleSlots];   // SWAP: a block's scales are in its slot
+  uint64_t sempty[kScaleSlots];  //       its block has been promoted
   uint64_t acc_full[kMaxBufs];
   uint64_t acc_empty[kMaxBufs];
   uint64_t mma_done;
   uint32_t tmem_addr;
   volatile int err;
 };
+
+// !SWAP: 168 registers a thread (384 threads) do not hold 128 accumulators and
+// the loads in flight, and a spill costs a trip to L2 (shared memory leaves no
+// L1), so the promotion warps take over registers of the other warpgroup:
+// 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kRegsMore = 224, kRegsLess = 56;
 
 template <bool SWAP_, int BN_, int PW_>
 struct Cfg {
@@ -76,23 +86,46 @@ struct Cfg {
   static constexpr uint32_t TMEM = NBUF * BN < 32 ? 32 : NBUF * BN;
   static constexpr int COLS = BN / (PW / 4);  // accumulator columns of one thread
   static constexpr int TOK = SWAP ? BN : kRows, WROWS = SWAP ? kRows : BN;
-  static constexpr int SW = WROWS / 128;      // weight scales per block
-  static constexpr int SLOT = TOK + 4;        // floats of a scale slot: token scales, then weight scales
+  static constexpr int LD = SWAP ? 16 : 32;
+  static constexpr int LDBUF = 2;  // 32-column register buffers of a promotion warp
+  static constexpr int SLOT = TOK + 4;        // floats of a scale slot: token scales, then the weight scale
   static constexpr int STAGE = (kRows + BN) * kBlockK;
-  static constexpr int THREADS = (PW + 2) * 32;
+  static constexpr int THREADS = (PW + 4) * 32;
   static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
-  static constexpr int EPI = SWAP ? 0 : PW * 2048;
-  static constexpr int FIXED = EPI + kScaleSlots * SLOT * 4 + (int)sizeof(Bars) + 1024;
+  static constexpr int EPI = SWAP ? 0 : PW * 1024;
+  static constexpr int SCALES = SWAP ? kScaleSlots * SLOT * 4 : 0;
+  static constexpr int FIXED = EPI + SCALES + (int)sizeof(Bars) + 1024;
 };
 
+// The same by one thread.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Bars* bars) {
-  if (bars->err) return false;
-  if (ptx::mbar_wait(bar, parity, kWaitLimitNs)) return true;
-  if (!bars->err) {
-    bars->err = 1;
-    atomicAdd(&g_fp8_wait_timeouts, 1u);
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (bars->err) return false;
+    if (clock64() - t0 > kWaitClocks) {
+      bars->err = 1;
+      atomicAdd(&g_fp8_wait_timeouts, 1u);
+      return false;
+    }
   }
-  return false;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// The warp waits for the phase (all lanes poll: one lane's tries took longer);
+// the vote makes the answer the warp's, so that code after it stays convergent.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars) {
+  const bool ok = __all_sync(0xFFFFFFFFu, wait_or_fail(bar, parity, bars));
+  __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -123,22 +156,81 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 // Wait for this thread's tensor-memory loads; the registers pass through, so
 // nothing that reads them moves above it.
-__device__ __forceinline__ void ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+template <int N>
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[N]) {
+  ptx::tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// a += t * s on pairs of fp32
-__device__ __forceinline__ void fma2(float2& a, uint32_t t0, uint32_t t1, float2 s) {
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
-      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "+f"(a.x), "+f"(a.y)
-      : "r"(t0), "r"(t1), "f"(s.x), "f"(s.y));
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { ptx::tmem_ld_16cols(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
+  ptx::tmem_ld_16cols(addr, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+  ptx::tmem_ld_16cols(addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
 }
+
+// Pairs of fp32 in a 64-bit register, for the packed fp32 arithmetic.
+__device__ __forceinline__ uint64_t pack_f32(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpack_f32(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// a += (t0, t1) * s
+__device__ __forceinline__ void fma2(uint64_t& a, uint32_t t0, uint32_t t1, uint64_t s) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"
+      : "+l"(a)
+      : "r"(t0), "r"(t1), "l"(s));
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+
+// The scale sx[m, kb] * sw[n / 128, kb] of one thread's row and columns, block by
+// block: four blocks are held, and the next four loaded while they are used.
+// (Every lane of a warp has its own row, so a load touches 32 sectors; through a
+// warp that copied them into shared memory block by block it took longer than
+// the block's MMAs.)
+struct ScaleStream {
+  const float *x, *w;
+  float4 have, nx, nw;
+  bool vec;
+  __device__ __forceinline__ void fetch(int kb, int kbs) {
+    if (vec) {  // rows of whole 16-byte groups
+      nx = __ldg(reinterpret_cast<const float4*>(x + kb));
+      nw = __ldg(reinterpret_cast<const float4*>(w + kb));
+    } else {
+      const int b = min(kb + 1, kbs - 1), c = min(kb + 2, kbs - 1), d = min(kb + 3, kbs - 1);
+      nx = make_float4(__ldg(x + kb), __ldg(x + b), __ldg(x + c), __ldg(x + d));
+      nw = make_float4(__ldg(w + kb), __ldg(w + b), __ldg(w + c), __ldg(w + d));
+    }
+  }
+  __device__ __forceinline__ void start(const float* x_, const float* w_, int kbs, bool vec_) {
+    x = x_;
+    w = w_;
+    vec = vec_;
+    fetch(0, kbs);
+  }
+  __device__ __forceinline__ float next(int kb, int kbs) {
+    if ((kb & 3) == 0) {
+      have = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
+      if (kb + 4 < kbs) fetch(kb + 4, kbs);
+    }
+    const float v = have.x;
+    have.x = have.y;
+    have.y = have.z;
+    have.z = have.w;
+    return v;
+  }
+};
 
 // One output tile: its expert's weight rows from w0, tokens [m0, mend).
 struct Tile {
@@ -149,7 +241,7 @@ struct Tile {
 // tiles; within a group, weight tile by weight tile.  Neighbouring CTAs so share
 // weight tiles, and a group's tokens stay in L2.  pre (grouped): token tiles
 // before each expert; off: its first row (E + 1 each).
-template <int TOK, int WROWS>
+template <int TILE, int WROWS>
 __device__ __forceinline__ Tile tile_of(int t, const Args& a, const int* pre, const int* off) {
   Tile r;
   int lo = 0, mt, first = 0, mend = a.T;
@@ -165,17 +257,62 @@ __device__ __forceinline__ Tile tile_of(int t, const Args& a, const int* pre, co
     first = off[lo];
     mend = off[a.E + 1 + lo];
   } else {
-    mt = (a.T + TOK - 1) / TOK;
+    mt = (a.T + TILE - 1) / TILE;
   }
   const int group = t / (kGroupTiles * a.nt);
   const int in = min(kGroupTiles, mt - group * kGroupTiles);
   t -= group * kGroupTiles * a.nt;
   const int n = t / in;
   r.e = lo;
-  r.m0 = first + (group * kGroupTiles + t - n * in) * TOK;
+  r.m0 = first + (group * kGroupTiles + t - n * in) * TILE;
   r.mend = mend;
   r.n0 = n * WROWS;
   return r;
+}
+
+// Stores COLS columns of the warp's 32 tokens (one per lane) from column n0 on,
+// through 1 KB of shared memory so that lanes store neighbouring columns.
+template <int COLS>
+__device__ __forceinline__ void store_rows(const Args& a, const uint64_t (&acc)[COLS / 2], uint8_t* stg, int m0, int mend,
+                                           int n0, int lane) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.Y) & 15u) == 0) && (a.ldy & 7) == 0;
+#pragma unroll
+  for (int c = 0; c < COLS / 16; ++c) {
+    // 16 columns (32 bytes) of each token; the two 16-byte halves change places
+    // every four tokens, against bank conflicts
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __float22bfloat162_rn(unpack_f32(acc[8 * c + i]));
+      o[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    uint8_t* mine = stg + lane * 32;
+    const int sw = (lane >> 2) & 1;
+    *reinterpret_cast<uint4*>(mine + 16 * sw) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(mine + 16 * (sw ^ 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    __syncwarp();
+    const int n = n0 + 16 * c;
+    if (vec && n + 16 <= a.N) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * i + (lane >> 1), p = lane & 1;
+        if (m0 + r < mend)
+          *reinterpret_cast<uint4*>(a.Y + (int64_t)(m0 + r) * a.ldy + n + 8 * p) =
+              *reinterpret_cast<const uint4*>(stg + r * 32 + 16 * (p ^ ((r >> 2) & 1)));
+      }
+    } else {
+      // rows at any address: two tokens at a time, a column per lane
+      const int k = lane & 15;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (m0 + r < mend && n + k < a.N)
+          a.Y[(int64_t)(m0 + r) * a.ldy + n + k] =
+              *reinterpret_cast<const uint16_t*>(stg + r * 32 + 16 * ((k >> 3) ^ ((r >> 2) & 1)) + 2 * (k & 7));
+      }
+    }
+    __syncwarp();
+  }
 }
 
 template <class C>
@@ -189,11 +326,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   uint8_t* smem = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
   uint8_t* epi = smem + a.stages * C::STAGE;
   float* scales = reinterpret_cast<float*>(epi + C::EPI);
-  Bars* bars = reinterpret_cast<Bars*>(scales + kScaleSlots * C::SLOT);
+  Bars* bars = reinterpret_cast<Bars*>(epi + C::EPI + C::SCALES);
   int* pre = reinterpret_cast<int*>(bars + 1);  // grouped: [E + 1] token tiles before
   int* off = pre + a.E + 1;                     // then [E + 1] first rows, [E + 1] row ends
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = a.splits > 1 ? (int)ptx::cluster_ctarank() : 0;
   const int kb0 = (int)((int64_t)a.kb * rank / a.splits), kb1 = (int)((int64_t)a.kb * (rank + 1) / a.splits);
   const int S = a.stages;
@@ -203,7 +340,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       ptx::mbar_init(&bars->full[i], 1);
       ptx::mbar_init(&bars->empty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) ptx::mbar_init(&bars->sfull[i], 32);
+    for (int i = 0; SWAP && i < kScaleSlots; ++i) {
+      ptx::mbar_init(&bars->sfull[i], 32);
+      ptx::mbar_init(&bars->sempty[i], PW);
+    }
     for (int i = 0; i < NBUF; ++i) {
       ptx::mbar_init(&bars->acc_full[i], 1);
       ptx::mbar_init(&bars->acc_empty[i], PW);
@@ -277,48 +417,56 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int tiles = a.nt * (a.offsets ? pre[a.E] : (a.T + C::TOK - 1) / C::TOK);
   const int first = blockIdx.x / a.splits, step = gridDim.x / a.splits;
 
-  if (warp == PW) {
-    // ---------------------------------------------------------------- producer
-    int st = 0, ph = 0, slot = 0;  // ph: parity that `empty` completes next
-    bool fresh = true;             // the ring's first pass: every stage is free
-    bool waited = a.offsets != nullptr;
-    int issued = 0;
-    for (int t = first; t < tiles; t += step) {
-      const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
-      const int wrow = w.e * a.N + w.n0;
-      const int wsrow = w.e * ((a.N + 127) / 128) + w.n0 / 128;
-      auto issue_w = [&](int s, int kb) {
-        ptx::tma_load_2d(smem + s * C::STAGE + (SWAP ? 0 : kRows * kBlockK), &tmap_w, &bars->full[s], kb * kBlockK,
-                         wrow);
-      };
-      int ahead = 0;  // stages whose weights are already on the way
-      if (!waited) {
-        ahead = a.static_weights ? min(S, kb1 - kb0) : 0;
-        if (lane == 0)
-          for (int i = 0; i < ahead; ++i) {
-            ptx::mbar_arrive_expect_tx(&bars->full[i], C::STAGE);
-            issue_w(i, kb0 + i);
-          }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        waited = true;
-      }
+  if (warp >= PW) {
+   if constexpr (!SWAP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
+   if (warp == PW || warp == PW + 3) {
+    // --------------------------------------------------------------- producers
+    // One thread for the tokens' tiles, one for the weights'.  (A wait, the
+    // barrier's byte count and two loads of one thread took longer than the
+    // block's MMAs.)
+    const bool weights = warp == PW + 3;
+    if (lane == 0) {
+      // with static weights theirs stream before the preceding work is done
+      if (!a.offsets && !(weights && a.static_weights)) asm volatile("griddepcontrol.wait;" ::: "memory");
+      const CUtensorMap* map = weights ? &tmap_w : &tmap_x;
+      uint8_t* const dst0 = smem + (SWAP == weights ? 0 : kRows * kBlockK);  // operand A is first
+      int st = 0, ph = 0, issued = 0;  // ph: parity that `empty` completes next
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!fresh && !__all_sync(0xFFFFFFFFu, wait_or_fail(&bars->empty[st], ph, bars))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          if (kb - kb0 >= ahead) {
-            ptx::mbar_arrive_expect_tx(&bars->full[st], C::STAGE);
-            issue_w(st, kb);
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
+        const int row = weights ? w.e * a.N + w.n0 : w.m0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (issued >= S && !wait_or_fail(&bars->empty[st], ph, bars)) {
+            ok = false;
+            break;
           }
-          ptx::tma_load_2d(smem + st * C::STAGE + (SWAP ? kRows * kBlockK : 0), &tmap_x, &bars->full[st],
-                           kb * kBlockK, w.m0);
+          if (!weights) ptx::mbar_arrive_expect_tx(&bars->full[st], C::STAGE);
+          ptx::tma_load_2d(dst0 + st * C::STAGE, map, &bars->full[st], kb * kBlockK, row);
+          ++issued;
+          if (++st == S) {
+            st = 0;
+            if (issued > S) ph ^= 1;
+          }
         }
-        // A slot is written again only after its block was promoted: this stage
-        // is free, so the MMAs of block g - stages are done, which could start
-        // once block g - stages - NBUF was promoted; there are more slots than that.
+      }
+      if (bars->err && !weights) {
+        // let the tiles already asked for land before the CTA exits
+        for (int g = max(issued - S, 0); g < issued; ++g) ptx::mbar_wait(&bars->full[g % S], (g / S) & 1, kDrainNs);
+      }
+    }
+    __syncwarp();
+   } else if (SWAP && warp == PW + 2) {
+    // ------------------------------------------------------------------ scales
+    // each block's token scales and weight scale into the next slot
+    int slot = 0, ph = 1;
+    bool ok = true;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
+      const float* sw = a.sw + (int64_t)(w.e * ((a.N + 127) / 128) + w.n0 / 128) * a.kb;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = warp_wait(&bars->sempty[slot], ph, bars);
+        if (!ok) break;
         float* d = scales + slot * C::SLOT;
 #pragma unroll
         for (int i = 0; i < (C::TOK + 31) / 32; ++i) {
@@ -326,161 +474,134 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (C::TOK % 32 == 0 || j < C::TOK)
             cp_async4(d + j, a.sx + (int64_t)min(m, a.T - 1) * a.kb + kb, m < a.T);
         }
-        if (lane < C::SW)
-          cp_async4(d + C::TOK + lane,
-                    a.sw + (int64_t)min(wsrow + lane, a.E * ((a.N + 127) / 128) - 1) * a.kb + kb,
-                    w.n0 + 128 * lane < a.N);
+        if (lane == 0) cp_async4(d + C::TOK, sw + kb, true);
         cp_async_arrive(&bars->sfull[slot]);
-        ++issued;
-        if (++slot == kScaleSlots) slot = 0;
-        if (++st == S) {
-          st = 0;
-          if (fresh) fresh = false; else ph ^= 1;
-        }
+        if (++slot == kScaleSlots) slot = 0, ph ^= 1;
       }
-      if (!ok) break;
     }
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (bars->err && lane == 0) {
-      // let the tiles already asked for land before the CTA exits
-      for (int g = max(issued - S, 0); g < issued; ++g) ptx::mbar_wait(&bars->full[g % S], (g / S) & 1, kWaitLimitNs);
-    }
-  } else if (warp == PW + 1) {
+   } else if (warp == PW + 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int st = 0, ph = 0, buf = 0, bph = 1;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          // (parity 1 passes at once on a fresh barrier: every buffer starts free)
-          if (!wait_or_fail(&bars->acc_empty[buf], bph, bars) || !wait_or_fail(&bars->full[st], ph, bars)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t a0 = ptx::smem_u32(smem + st * C::STAGE), b0 = a0 + kRows * kBlockK;
+    // (the whole warp walks the blocks and one elected lane issues: in a branch
+    // of one lane the descriptors would have to be moved to uniform registers
+    // before every MMA)
+    int st = 0, ph = 0, buf = 0, bph = 1;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        // (parity 1 passes at once on a fresh barrier: every buffer starts free)
+        ok = warp_wait(&bars->full[st], ph, bars) && warp_wait(&bars->acc_empty[buf], bph, bars);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t a0 = ptx::smem_u32(smem) + st * C::STAGE, b0 = a0 + kRows * kBlockK;
+        const uint64_t da = ptx::sw128_kmajor_desc(a0), db = ptx::sw128_kmajor_desc(b0);
+        const uint32_t d = tmem + buf * BN;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f8(tmem + buf * BN, ptx::sw128_kmajor_desc(a0 + 32 * kk), ptx::sw128_kmajor_desc(b0 + 32 * kk), kIdesc,
-                   kk != 0);
-          ptx::mma_commit(&bars->empty[st]);
+          for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
+            mma_f8(d, da + 2 * kk, db + 2 * kk, kIdesc, kk != 0);
           ptx::mma_commit(&bars->acc_full[buf]);
-          if (++st == S) st = 0, ph ^= 1;
-          if (++buf == NBUF) buf = 0, bph ^= 1;
+          ptx::mma_commit(&bars->empty[st]);
         }
+        __syncwarp();
+        if (++st == S) st = 0, ph ^= 1;
+        if (++buf == NBUF) buf = 0, bph ^= 1;
       }
-      // arrives when every MMA above is done, so that tensor memory is never
-      // freed under one (also on the error path)
-      ptx::mma_commit(&bars->mma_done);
-      ptx::mbar_wait(&bars->mma_done, 0, kWaitLimitNs);
     }
+    // arrives when every MMA above is done, so that tensor memory is never
+    // freed under one (also on the error path)
+    if (elect_one()) ptx::mma_commit(&bars->mma_done);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_wait(&bars->mma_done, 0, kDrainNs);
+    __syncwarp();
+   }
   } else {
     // --------------------------------------------------------------- promotion
+    static_assert(SWAP || PW == 8, "registers are split for eight promotion warps");
+    if constexpr (!SWAP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
     const int quarter = warp & 3, part = warp >> 2;
     const int row = 32 * quarter + lane, col0 = part * COLS;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16) + col0;
     int buf = 0, bph = 0, slot = 0, sph = 0;
     bool ok = true;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // Y
+    [[maybe_unused]] const bool scale_vec =
+        a.kb % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.sx) | reinterpret_cast<uintptr_t>(a.sw)) & 15) == 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the scales and Y
     for (int t = first; t < tiles && ok; t += step) {
-      float2 acc[COLS / 2];
+      uint64_t acc[COLS / 2];
 #pragma unroll
-      for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+      for (int j = 0; j < COLS / 2; ++j) acc[j] = 0;
+      const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
+      [[maybe_unused]] ScaleStream scale;
+      if constexpr (!SWAP) {
+        const int m = min(w.m0 + row, a.T - 1);
+        const int nb = (a.N + 127) / 128, n = min(w.n0 / 128 + part, nb - 1);
+        scale.start(a.sx + (int64_t)m * a.kb, a.sw + (int64_t)(w.e * nb + n) * a.kb, a.kb, scale_vec);
+      }
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!__all_sync(0xFFFFFFFFu,
-                        wait_or_fail(&bars->sfull[slot], sph, bars) && wait_or_fail(&bars->acc_full[buf], bph, bars))) {
-          ok = false;
-          break;
+        uint64_t srow = 0, sw2 = 0;
+        const float* sc = nullptr;
+        if constexpr (SWAP) {
+          ok = warp_wait(&bars->sfull[slot], sph, bars) && warp_wait(&bars->acc_full[buf], bph, bars);
+          sc = scales + slot * C::SLOT;
+          sw2 = pack_f32(sc[C::TOK], sc[C::TOK]);
+        } else {
+          const float v = scale.next(kb, a.kb);
+          srow = pack_f32(v, v);
+          ok = warp_wait(&bars->acc_full[buf], bph, bars);
         }
+        if (!ok) break;
         ptx::tc_fence_after();
-        const float* sc = scales + slot * C::SLOT;
-        const float sw = sc[C::TOK + (SWAP ? 0 : col0 / 128)];
-        const float srow = SWAP ? 0.0f : sc[row] * sw;
-        uint32_t r[2][16];
-        ptx::tmem_ld_16cols(lane_addr + buf * BN, r[0]);
+        constexpr int LD = COLS < C::LD ? COLS : C::LD, NLD = COLS / LD, NR = NLD < C::LDBUF ? NLD : C::LDBUF;
+        uint32_t r[NR][LD];
+        tmem_ld(lane_addr + buf * BN, r[0]);
 #pragma unroll
-        for (int c = 0; c < COLS / 16; ++c) {
-          ld_wait16(r[c & 1]);
-          if (c + 1 < COLS / 16) ptx::tmem_ld_16cols(lane_addr + buf * BN + 16 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float2 s;
-            if (SWAP) {
-              s = *reinterpret_cast<const float2*>(sc + col0 + 16 * c + 2 * j);
-              s.x *= sw;
-              s.y *= sw;
-            } else {
-              s = make_float2(srow, srow);
-            }
-            fma2(acc[8 * c + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], s);
+        for (int c = 0; c < NLD; ++c) {
+          ld_wait(r[c % NR]);
+          if (c + 1 == NLD) {  // all of it read: the MMAs may have the accumulator back
+            ptx::tc_fence_before();
+            if (elect_one()) ptx::mbar_arrive(&bars->acc_empty[buf]);
           }
+          if (NR > 1 && c + 1 < NLD) tmem_ld(lane_addr + buf * BN + LD * (c + 1), r[(c + 1) % NR]);
+#pragma unroll
+          for (int j = 0; j < LD / 2; ++j) {
+            const uint64_t s =
+                SWAP ? mul2(*reinterpret_cast<const uint64_t*>(sc + col0 + LD * c + 2 * j), sw2) : srow;
+            fma2(acc[LD / 2 * c + j], r[c % NR][2 * j], r[c % NR][2 * j + 1], s);
+          }
+          if (NR == 1 && c + 1 < NLD) tmem_ld(lane_addr + buf * BN + LD * (c + 1), r[0]);
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars->acc_empty[buf]);
         if (++buf == NBUF) buf = 0, bph ^= 1;
-        if (++slot == kScaleSlots) slot = 0, sph ^= 1;
+        if constexpr (SWAP) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->sempty[slot]);
+          if (++slot == kScaleSlots) slot = 0, sph ^= 1;
+        }
       }
       if (!ok) break;
-      const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
       if constexpr (SWAP) {
         if (a.splits > 1) {
           // partial sums to the (now idle) stage memory, [token][weight row]
           float* part_sum = reinterpret_cast<float*>(smem);
 #pragma unroll
           for (int j = 0; j < COLS / 2; ++j) {
-            part_sum[(col0 + 2 * j) * kRows + row] = acc[j].x;
-            part_sum[(col0 + 2 * j + 1) * kRows + row] = acc[j].y;
+            const float2 v = unpack_f32(acc[j]);
+            part_sum[(col0 + 2 * j) * kRows + row] = v.x;
+            part_sum[(col0 + 2 * j + 1) * kRows + row] = v.y;
           }
         } else if (w.n0 + row < a.N) {
 #pragma unroll
           for (int j = 0; j < COLS; ++j) {
             const int m = w.m0 + col0 + j;
             if (m < w.mend) {
-              const __nv_bfloat16 o = __float2bfloat16_rn(j & 1 ? acc[j / 2].y : acc[j / 2].x);
+              const __nv_bfloat16 o = __float2bfloat16_rn(j & 1 ? unpack_f32(acc[j / 2]).y : unpack_f32(acc[j / 2]).x);
               a.Y[(int64_t)m * a.ldy + w.n0 + row] = *reinterpret_cast<const uint16_t*>(&o);
             }
           }
         }
       } else {
-        // through shared memory, 32 columns (64 bytes) of the warp's 32 tokens at
-        // a time, so that four lanes store one token's 64 bytes; the 16-byte
-        // pieces are rotated by the row against bank conflicts
-        uint8_t* stg = epi + warp * 2048;
-        const bool vec = ((reinterpret_cast<uintptr_t>(a.Y) & 15u) == 0) && (a.ldy & 7) == 0;
-#pragma unroll
-        for (int c = 0; c < COLS / 32; ++c) {
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 h = __float22bfloat162_rn(acc[16 * c + 4 * p + i]);
-              o[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(stg + lane * 64 + ((p + (lane >> 1)) & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), p = lane & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 64 + ((p + (rr >> 1)) & 3) * 16);
-            const int m = w.m0 + 32 * quarter + rr, n = w.n0 + col0 + 32 * c + 8 * p;
-            if (m < w.mend && n < a.N) {
-              uint16_t* dst = a.Y + (int64_t)m * a.ldy + n;
-              if (vec && n + 8 <= a.N) {
-                *reinterpret_cast<uint4*>(dst) = v;
-              } else {
-                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  if (n + k < a.N) dst[k] = (uint16_t)(w4[k >> 1] >> (16 * (k & 1)));
-              }
-            }
-          }
-          __syncwarp();
-        }
+        store_rows<COLS>(a, acc, epi + warp * 1024, w.m0 + 32 * quarter, w.mend,
+                         w.n0 + col0, lane);
       }
     }
   }
@@ -515,46 +636,144 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   }
 }
 
-constexpr int kSmemMax = 232448;  // dynamic shared memory of a CTA that has the SM to itself
-constexpr int kSmemHalf = 115712; // of one that shares it with another
-
-template <class C>
-cudaError_t run(const uint8_t* x, const uint8_t* w, Args a, int sms, int64_t tiles, cudaStream_t stream) {
-  static tc::SmemOptIn opt;
-  const int table = a.offsets ? 3 * (a.E + 1) * 4 : 0;
-  const int room = (C::CTAS == 2 ? kSmemHalf : kSmemMax) - C::FIXED - table;
-  a.stages = room / C::STAGE < kMaxStages ? room / C::STAGE : kMaxStages;
-  if (a.stages < 2) return cudaErrorInvalidConfiguration;
-  static_assert(kMaxStages + C::NBUF <= kScaleSlots, "scale slots outlive stages and accumulators");
-  CUtensorMap mw, mx;
-  if (!tc::make_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)a.K, (uint64_t)a.E * a.N, (uint64_t)a.K,
-                        kBlockK, C::WROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tc::make_tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K, kBlockK,
-                        C::TOK, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  const int smem = C::FIXED + table + a.stages * C::STAGE;
-  const void* fn = (const void*)fp8_gemm_kernel<C>;
-  cudaError_t e = opt.ensure(fn, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t slots = (int64_t)sms * C::CTAS;
-  const int64_t grid = a.splits > 1 ? tiles * a.splits : (tiles < slots ? tiles : slots);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)a.splits, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  void* args[] = {&mw, &mx, &a};
-  return cudaLaunchKernelExC(&cfg, fn, args);
-}
+constexpr int kSmemMax = 232448;   // dynamic shared memory of a CTA that has the SM to itself
+constexpr int kSmemHalf = 115712;  // of one that shares it with another
 
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+template <class C>
+int stages_of(int table) {
+  const int n = ((C::CTAS == 2 ? kSmemHalf : kSmemMax) - C::FIXED - table) / C::STAGE;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
+// CTAs of clusters of c that run at once (a cluster stays within one GPC, so a
+// few SMs are left over), asked of the driver once per device and size.
+template <class C>
+int64_t resident(int c, int sms) {
+  if (c == 1) return (int64_t)sms * C::CTAS;
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][c].load();
+  if (n == 0) {
+    static tc::SmemOptIn opt;
+    const void* fn = (const void*)fp8_gemm_kernel<C>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::FIXED + stages_of<C>(0) * C::STAGE;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)c, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (opt.ensure(fn, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // no clusters of this size then
+      return 0;
+    }
+    n = clusters * c;
+    known[dev][c].store(n);
+  }
+  return n;
+}
+
+struct Problem {
+  const uint8_t* x;
+  const uint8_t* w;
+  Args a;
+  int64_t active;  // experts that may have rows, 0: dense
+  int sms;
+  cudaStream_t stream;
+
+  // Token tiles of `tok` rows: of a grouped call an estimate (half a tile per
+  // expert is empty), or the most there can be.
+  template <class C>
+  int64_t tiles(bool most) const {
+    const int64_t mt = a.offsets ? a.T / C::TOK + (most ? a.E : (active + 1) / 2) : cdiv(a.T, C::TOK);
+    return mt * cdiv(a.N, C::WROWS);
+  }
+
+  // Estimated microseconds of a configuration with c CTAs sharing each tile's k:
+  // waves of CTAs times blocks of k, at least the time to read the weights.
+  // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
+  // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
+  // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
+  // 0.8 and 0.025 per token of the tile.  The choices by this rule run within 15%
+  // of the best one of each shape there, mostly within 5%; by tile width alone
+  // (M <= 16: 16 tokens, and so on) they were up to 2.7 times slower.
+  template <class C>
+  double estimate(int c) const {
+    constexpr double alone = C::BN == 16 ? 0.19 : C::BN == 32 ? 0.24 : C::BN == 64 ? 0.40 : C::BN == 128 ? 0.38 : 0.40;
+    constexpr double full = C::BN == 16 ? 0.29 : C::BN == 32 ? 0.36 : C::BN == 64 ? 0.52 : C::BN == 128 ? 0.45 : 0.51;
+    constexpr double store = C::BN == 16 ? 0.5 : C::BN == 32 ? 0.7 : C::BN == 64 ? 1.0 : 1.5;
+    const int64_t slots = resident<C>(c, sms), ctas = tiles<C>(false) * c;
+    if (slots == 0) return 1e30;
+    const double per_block = ctas > (C::BN >= 128 ? 100 : sms) ? full : alone;
+    const double work = (double)cdiv(ctas, slots) * ((double)cdiv(a.kb, c) * per_block + store);
+    const double bytes = (double)(active ? active : 1) * a.N * a.K + (double)a.T * (a.K + 2.0 * a.N);
+    return (work > bytes / 6.3e6 ? work : bytes / 6.3e6) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
+  }
+
+  template <class C>
+  void consider(double& best, int& bn, int& splits) const {
+    if (stages_of<C>(a.offsets ? 3 * (a.E + 1) * 4 : 0) < 2) return;
+    // (a grouped call's tiles are not known here, so a cluster per tile cannot be)
+    const int most = C::SWAP && !a.offsets ? (a.kb < 8 ? a.kb : 8) : 1;
+    for (int c = 1; c <= most; ++c) {
+      if (c > 1 && tiles<C>(true) * c > 4 * (int64_t)sms) break;  // enough tiles to fill the GPU
+      const double t = estimate<C>(c);
+      if (t < best) {
+        best = t;
+        bn = C::BN;
+        splits = c;
+      }
+    }
+  }
+
+  template <class C>
+  cudaError_t run(int splits) const {
+    static tc::SmemOptIn opt;
+    Args b = a;
+    b.splits = splits;
+    b.nt = (int)cdiv(a.N, C::WROWS);
+    const int table = a.offsets ? 3 * (a.E + 1) * 4 : 0;
+    b.stages = stages_of<C>(table);
+    CUtensorMap mw, mx;
+    if (!tc::make_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)a.K, (uint64_t)a.E * a.N, (uint64_t)a.K,
+                          kBlockK, C::WROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tc::make_tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K, kBlockK,
+                          C::TOK, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    const int smem = C::FIXED + table + b.stages * C::STAGE;
+    const void* fn = (const void*)fp8_gemm_kernel<C>;
+    cudaError_t e = opt.ensure(fn, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t n = tiles<C>(true), slots = (int64_t)sms * C::CTAS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(splits > 1 ? n * splits : n < slots ? n : slots));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)splits, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    void* args[] = {&mw, &mx, &b};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+  }
+};
+
+using S16 = Cfg<true, 16, 4>;
+using S32 = Cfg<true, 32, 4>;
+using S64 = Cfg<true, 64, 4>;
+using S128 = Cfg<true, 128, 8>;
+using L256 = Cfg<false, 256, 8>;
 
 }  // namespace
 
@@ -572,35 +791,23 @@ cudaError_t launch_fp8_gemm(const uint8_t* x, const float* sx, const uint8_t* w,
   a.K = (int)K;
   a.E = (int)E;
   a.kb = (int)cdiv(K, kBlockK);
-  a.splits = 1;
   a.static_weights = static_weights;
-  const int64_t rows = offsets ? cdiv(T, E) : T;  // per expert, on average
-  if (rows > 128 && cdiv(rows, 128) * cdiv(N, 256) * E >= 120) {
-    a.nt = (int)cdiv(N, 256);
-    const int64_t most = a.nt * (offsets ? T / 128 + E : cdiv(T, 128));
-    return run<Cfg<false, 256, 8>>(x, w, a, sms, most, stream);
-  }
-  const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  const int per_sm = bn <= 64 ? 2 : 1;
-  a.nt = (int)cdiv(N, 128);
-  const int64_t tiles = a.nt * (offsets ? T / bn + E : cdiv(T, bn));
-  if (!offsets) {
-    // fewest waves times blocks of k per CTA
-    int64_t best = 0;
-    for (int c = 1; c <= 8 && c <= a.kb; ++c) {
-      const int64_t cost = cdiv(tiles * c, (int64_t)sms * per_sm) * (cdiv(a.kb, c) + 2) + (c > 1 ? 2 : 0);
-      if (c == 1 || cost < best) {
-        best = cost;
-        a.splits = c;
-      }
-    }
-  }
+  const Problem p{x, w, a, offsets ? (E < T ? E : T) : 0, sms, stream};
+  double best = 1e300;
+  int bn = 0, splits = 1;
+  p.consider<S16>(best, bn, splits);
+  p.consider<S32>(best, bn, splits);
+  p.consider<S64>(best, bn, splits);
+  p.consider<S128>(best, bn, splits);
+  p.consider<L256>(best, bn, splits);
   switch (bn) {
-    case 16: return run<Cfg<true, 16, 4>>(x, w, a, sms, tiles, stream);
-    case 32: return run<Cfg<true, 32, 4>>(x, w, a, sms, tiles, stream);
-    case 64: return run<Cfg<true, 64, 4>>(x, w, a, sms, tiles, stream);
-    default: return run<Cfg<true, 128, 8>>(x, w, a, sms, tiles, stream);
+    case 16: return p.run<S16>(splits);
+    case 32: return p.run<S32>(splits);
+    case 64: return p.run<S64>(splits);
+    case 128: return p.run<S128>(splits);
+    case 256: return p.run<L256>(splits);
   }
+  return cudaErrorInvalidConfiguration;
 }
 
 cudaError_t read_and_clear_fp8_errors(unsigned int* timeouts, unsigned int* bad_offsets) {
