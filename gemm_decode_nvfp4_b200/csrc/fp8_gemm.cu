@@ -26,8 +26,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -647,37 +645,15 @@ int stages_of(int table) {
   return n < kMaxStages ? n : kMaxStages;
 }
 
-// CTAs of clusters of c that run at once (a cluster stays within one GPC, so a
-// few SMs are left over), asked of the driver once per device and size.
+// CTAs of clusters of c that run at once.  A cluster stays within one GPC, so a
+// few SMs are left over; in thousandths of the SMs, as the occupancy of an empty
+// kernel with this shared memory has it on one B200 (148 SMs).  (Of this kernel
+// the driver reports one CTA per SM whatever its size, but two do run.)
 template <class C>
 int64_t resident(int c, int sms) {
-  if (c == 1) return (int64_t)sms * C::CTAS;
-  static std::atomic<int> known[64][9];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = known[dev][c].load();
-  if (n == 0) {
-    static tc::SmemOptIn opt;
-    const void* fn = (const void*)fp8_gemm_kernel<C>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)c);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::FIXED + stages_of<C>(0) * C::STAGE;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)c, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (opt.ensure(fn, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess) {
-      cudaGetLastError();  // no clusters of this size then
-      return 0;
-    }
-    n = clusters * c;
-    known[dev][c].store(n);
-  }
-  return n;
+  constexpr int one[9] = {0, 1000, 1000, 912, 891, 878, 891, 709, 810};
+  constexpr int two[9] = {0, 1000, 1000, 942, 959, 945, 912, 875, 891};
+  return (int64_t)sms * C::CTAS * (C::CTAS == 2 ? two[c] : one[c]) / 1000;
 }
 
 struct Problem {
@@ -697,7 +673,8 @@ struct Problem {
   }
 
   // Estimated microseconds of a configuration with c CTAs sharing each tile's k:
-  // waves of CTAs times blocks of k, at least the time to read the weights.
+  // waves of CTAs times blocks of k, at least the time to read the weights
+  // (6.3 TB/s, which nine tenths of the SMs reach).
   // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
   // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
   // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
@@ -710,11 +687,11 @@ struct Problem {
     constexpr double full = C::BN == 16 ? 0.29 : C::BN == 32 ? 0.36 : C::BN == 64 ? 0.52 : C::BN == 128 ? 0.45 : 0.51;
     constexpr double store = C::BN == 16 ? 0.5 : C::BN == 32 ? 0.7 : C::BN == 64 ? 1.0 : 1.5;
     const int64_t slots = resident<C>(c, sms), ctas = tiles<C>(false) * c;
-    if (slots == 0) return 1e30;
     const double per_block = ctas > (C::BN >= 128 ? 100 : sms) ? full : alone;
     const double work = (double)cdiv(ctas, slots) * ((double)cdiv(a.kb, c) * per_block + store);
     const double bytes = (double)(active ? active : 1) * a.N * a.K + (double)a.T * (a.K + 2.0 * a.N);
-    return (work > bytes / 6.3e6 ? work : bytes / 6.3e6) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
+    const double stream = bytes / 6.3e6 * (ctas < 0.92 * sms ? 0.92 * sms / ctas : 1.0);
+    return (work > stream ? work : stream) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
   }
 
   template <class C>
