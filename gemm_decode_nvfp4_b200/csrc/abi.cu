@@ -550,6 +550,8 @@ nvfp4_status nvfp4_check_device_errors(void) {
   unsigned int f8 = 0, bad_offsets = 0;
   if (e == cudaSuccess) e = nvfp4::read_and_clear_fp8_errors(&f8, &bad_offsets);
   n += f8;
+  if (e == cudaSuccess) e = nvfp4::read_and_clear_fp8_norm_timeouts(&f8);
+  n += f8;
   if (e == cudaSuccess) e = nvfp4::read_and_clear_small_timeouts(&k);
   if (e == cudaSuccess) e = nvfp4::read_and_clear_gemv_timeouts(&v);
   unsigned int bad = 0, window = 0;

@@ -86,7 +86,7 @@ nvfp4_status fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* weight,
   int sms = 0;
   st = nvfp4::require_device(&sms);
   if (st != NVFP4_OK) return st;
-  return launched(nvfp4::launch_fp8_rmsnorm(x, ldx, weight, residual, ldr, residual_out, ldro, y, ldy, q, s, M, K, eps,
+  return launched(nvfp4::launch_fp8_rmsnorm(x, ldx, weight, residual, ldr, residual_out, ldro, y, ldy, q, s, M, K, eps, sms,
                                             (cudaStream_t)stream),
                   "rmsnorm launch");
 }

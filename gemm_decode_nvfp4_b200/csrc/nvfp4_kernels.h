@@ -114,7 +114,8 @@ nvfp4_status require_device(int* sms);
 // weight quantizer.
 cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* weight, const uint16_t* residual,
                                int64_t ldr, uint16_t* residual_out, int64_t ldro, uint16_t* y, int64_t ldy, uint8_t* q,
-                               float* s, int64_t M, int64_t K, float eps, cudaStream_t stream);
+                               float* s, int64_t M, int64_t K, float eps, int sms, cudaStream_t stream);
+cudaError_t read_and_clear_fp8_norm_timeouts(unsigned int* count);
 cudaError_t launch_fp8_quantize(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, bool gated, uint8_t* q, float* s,
                                 int sms, cudaStream_t stream);
 cudaError_t launch_fp8_quantize_weights(const uint16_t* w, int64_t ldw, int64_t N, int64_t K, uint8_t* q, float* s,

@@ -194,6 +194,29 @@ def test_rmsnorm(nv, M, K, residual):
     chk_q(), chk_s(), chk_y(), chk_r()
 
 
+@pytest.mark.parametrize("M,K", [(297, 1040), (700, 5120), (600, 8192), (900, 8208), (1200, 16384), (305, 17408),
+                                 (301, 32768), (2500, 272)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_many_rows(nv, M, K, residual):
+    """More rows than CTAs: each CTA takes several, out of strided tensors."""
+    wide = randn((M, K + 24), M + K)
+    x, w = wide[:, 8:8 + K], randn((K,), K)
+    r = randn((M, K + 8), M + K + 1, 3.0)[:, :K] if residual else None
+    h, v = norm_ref(x, r, w, 1e-6)
+    q, chk_q = guarded_empty((M, K), F8)
+    s, chk_s = guarded_empty((M, blocks(K)), F32)
+    y, chk_y = guarded_empty((M, K), BF16)
+    ro, chk_r = guarded_empty((M, K), BF16)
+    nv.fp8_rmsnorm(x, w, 1e-6, residual=r, residual_out=ro if residual else None, y=y, q=q, s=s)
+    check_y(v, y)
+    check_quantized(v, q, s, 2.0 ** -18)
+    if residual:
+        assert torch.equal(ro, h)
+        nv.fp8_rmsnorm(x, w, 1e-6, residual=r, y=y)      # in place
+        assert torch.equal(r, h)
+    chk_q(), chk_s(), chk_y(), chk_r()
+
+
 @pytest.mark.parametrize("K", [400, 5120, 40960])
 def test_rmsnorm_outputs_alone_and_in_place(nv, K):
     """y alone, (q, s) alone and the residual in place give what all together give."""
