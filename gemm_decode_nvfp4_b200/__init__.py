@@ -154,11 +154,12 @@ def _ptr(t: torch.Tensor | None):
 def _need(t: torch.Tensor, dtype, what: str, ndim=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if ndim is not None and t.dim() != ndim:
+    dim = t.dim()
+    if ndim is not None and dim != ndim:
         raise ValueError(f"{what} must be {ndim}-D, got shape {tuple(t.shape)}")
-    if t.dim() >= 1 and t.numel() > 0 and t.stride(-1) != 1:
+    if dim >= 1 and t.stride(-1) != 1 and t.numel() > 0:
         raise ValueError(f"{what} must be contiguous in its last dimension")
 
 
@@ -537,9 +538,9 @@ def _ld(t: torch.Tensor | None) -> int:
 
 
 def _need_fp8(q: torch.Tensor, s: torch.Tensor, what: str, shape: tuple, scale_shape: tuple):
-    """q float8_e4m3fn of `shape` and its scales s float32 of `scale_shape`, both contiguous."""
-    if not (q.dtype is _F8 and q.is_cuda and s.dtype is torch.float32 and s.is_cuda):
-        _need(q, _F8, what)
+    """q (checked to be a float8_e4m3fn CUDA tensor) of `shape` and its scales s
+    float32 of `scale_shape`, both contiguous."""
+    if not isinstance(s, torch.Tensor) or not s.is_cuda or s.dtype is not torch.float32:
         _need(s, torch.float32, f"{what}'s scales")
     if q.shape != shape or s.shape != scale_shape or not q.is_contiguous() or not s.is_contiguous():
         raise ValueError(f"{what} must be contiguous {list(shape)} with scales {list(scale_shape)}, got "
@@ -555,7 +556,8 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     q float8_e4m3fn [M, K] with s float32 [M, ceil(K/128)]."""
     _need(x, torch.bfloat16, "x", 2)
     _need(weight, torch.bfloat16, "weight", 1)
-    M, K = x.shape
+    shape = x.shape
+    M, K = shape
     if weight.shape[0] != K:
         raise ValueError(f"weight must hold K={K} elements, got {weight.shape[0]}")
     if residual is None and residual_out is not None:
@@ -565,12 +567,13 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     for t, what in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
         if t is not None:
             _need(t, torch.bfloat16, what, 2)
-            if t.shape != x.shape:
-                raise ValueError(f"{what} must be {tuple(x.shape)}, got {tuple(t.shape)}")
+            if t.shape != shape:
+                raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
     if (q is None) != (s is None):
         raise ValueError("q and s go together")
     if q is not None:
-        _need_fp8(q, s, "q", (M, K), (M, _blocks(K)))
+        _need(q, _F8, "q", 2)
+        _need_fp8(q, s, "q", shape, (M, _blocks(K)))
     dev = _device(x, weight, residual, residual_out, y, q, s)
     _call("fp8_rmsnorm", dev, _ptr(x), _ld(x), _ptr(weight), _ptr(residual), _ld(residual), _ptr(residual_out),
           _ld(residual_out), _ptr(y), _ld(y), _ptr(q), _ptr(s), M, K, float(eps), _stream(stream, dev))
@@ -584,6 +587,7 @@ def fp8_quantize(X: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gated: bool 
     if gated and cols % 2:
         raise ValueError(f"a gated X has an even number of columns, got {cols}")
     K = cols // 2 if gated else cols
+    _need(q, _F8, "q", 2)
     _need_fp8(q, s, "q", (M, K), (M, _blocks(K)))
     dev = _device(X, q, s)
     _call("fp8_quantize", dev, _ptr(X), _ld(X), M, K, _ptr(q), _ptr(s), FLAG_FP8_GATED if gated else 0,
@@ -594,6 +598,7 @@ def fp8_quantize_weights(W: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stre
     """BF16 weights W [N, K] into q float8_e4m3fn [N, K] and s float32 [ceil(N/128), ceil(K/128)]."""
     _need(W, torch.bfloat16, "W", 2)
     N, K = W.shape
+    _need(q, _F8, "q", 2)
     _need_fp8(q, s, "q", (N, K), (_blocks(N), _blocks(K)))
     dev = _device(W, q, s)
     _call("fp8_quantize_weights", dev, _ptr(W), _ld(W), N, K, _ptr(q), _ptr(s), _stream(stream, dev))
