@@ -126,6 +126,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* 
   return ok;
 }
 
+// four fp32 at the same shared-memory offset as `local` in the cluster's CTA `rank`
+__device__ __forceinline__ float4 ld_cluster_v4(const float* local, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(ptx::cluster_addr(local, rank))
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -618,14 +628,35 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       if (!bars->err && first < tiles) {
         const Tile w = tile_of<C::TOK, C::WROWS>(first, a, pre, off);
         const float* part_sum = reinterpret_cast<const float*>(smem);
-        const int live = min(BN, w.mend - w.m0) * kRows;
+        // four weight rows of one token at a time; all shares are asked for before
+        // the first is added
+        const int live = min(BN, w.mend - w.m0) * (kRows / 4);
+        const bool vec = ((reinterpret_cast<uintptr_t>(a.Y) & 7u) == 0) && (a.ldy & 3) == 0;
         for (int i = threadIdx.x + rank * C::THREADS; i < live; i += C::THREADS * a.splits) {
-          float v = 0.0f;
-          for (int r = 0; r < a.splits; ++r) v += ptx::ld_cluster_f32(part_sum + i, r);
-          const int m = w.m0 + i / kRows, n = w.n0 + i % kRows;
-          if (n < a.N) {
-            const __nv_bfloat16 o = __float2bfloat16_rn(v);
-            a.Y[(int64_t)m * a.ldy + n] = *reinterpret_cast<const uint16_t*>(&o);
+          float4 v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < a.splits) v[r] = ld_cluster_v4(part_sum + 4 * i, r);
+          float4 sum = v[0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r)
+            if (r < a.splits) {
+              sum.x += v[r].x;
+              sum.y += v[r].y;
+              sum.z += v[r].z;
+              sum.w += v[r].w;
+            }
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
+          const uint2 o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          const int m = w.m0 + i / (kRows / 4), n = w.n0 + 4 * (i % (kRows / 4));
+          uint16_t* dst = a.Y + (int64_t)m * a.ldy + n;
+          if (vec && n + 4 <= a.N) {
+            *reinterpret_cast<uint2*>(dst) = o;
+          } else {
+            if (n < a.N) dst[0] = (uint16_t)o.x;
+            if (n + 1 < a.N) dst[1] = (uint16_t)(o.x >> 16);
+            if (n + 2 < a.N) dst[2] = (uint16_t)o.y;
+            if (n + 3 < a.N) dst[3] = (uint16_t)(o.y >> 16);
           }
         }
       }
@@ -673,8 +704,9 @@ struct Problem {
   }
 
   // Estimated microseconds of a configuration with c CTAs sharing each tile's k:
-  // waves of CTAs times blocks of k, at least the time to read the weights
-  // (6.3 TB/s, which nine tenths of the SMs reach).
+  // waves of CTAs times blocks of k, and the time to read the weights
+  // (6.3 TB/s, which nine tenths of the SMs reach); the longer one counts in full,
+  // the other one, mostly behind it, a quarter.
   // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
   // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
   // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
@@ -691,7 +723,7 @@ struct Problem {
     const double work = (double)cdiv(ctas, slots) * ((double)cdiv(a.kb, c) * per_block + store);
     const double bytes = (double)(active ? active : 1) * a.N * a.K + (double)a.T * (a.K + 2.0 * a.N);
     const double stream = bytes / 6.3e6 * (ctas < 0.92 * sms ? 0.92 * sms / ctas : 1.0);
-    return (work > stream ? work : stream) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
+    return (work > stream ? work + 0.25 * stream : stream + 0.25 * work) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
   }
 
   template <class C>
@@ -748,8 +780,8 @@ struct Problem {
 
 using S16 = Cfg<true, 16, 4>;
 using S32 = Cfg<true, 32, 4>;
-using S64 = Cfg<true, 64, 4>;
-using S128 = Cfg<true, 128, 8>;
+using S64 = Cfg<true, 64, 8>;
+using S128 = Cfg<true, 128, 16>;
 using L256 = Cfg<false, 256, 8>;
 
 }  // namespace
