@@ -90,7 +90,7 @@ struct Cfg {
   static constexpr int STAGE = (kRows + BN) * kBlockK;
   static constexpr int THREADS = (PW + 4) * 32;
   static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
-  static constexpr int EPI = SWAP ? 0 : PW * 1024;
+  static constexpr int EPI = SWAP ? 0 : PW * 2048;
   static constexpr int SCALES = SWAP ? kScaleSlots * SLOT * 4 : 0;
   static constexpr int FIXED = EPI + SCALES + (int)sizeof(Bars) + 1024;
 };
@@ -279,45 +279,42 @@ __device__ __forceinline__ Tile tile_of(int t, const Args& a, const int* pre, co
 }
 
 // Stores COLS columns of the warp's 32 tokens (one per lane) from column n0 on,
-// through 1 KB of shared memory so that lanes store neighbouring columns.
+// through 2 KB of shared memory so that lanes store neighbouring columns.
 template <int COLS>
 __device__ __forceinline__ void store_rows(const Args& a, const uint64_t (&acc)[COLS / 2], uint8_t* stg, int m0, int mend,
                                            int n0, int lane) {
   const bool vec = ((reinterpret_cast<uintptr_t>(a.Y) & 15u) == 0) && (a.ldy & 7) == 0;
+  // 32 columns (64 bytes) of each token at a time; the 16-byte pieces of a row are
+  // rotated by half the row, against bank conflicts
+  auto piece = [&](int row, int p) { return stg + row * 64 + 16 * ((p + (row >> 1)) & 3); };
 #pragma unroll
-  for (int c = 0; c < COLS / 16; ++c) {
-    // 16 columns (32 bytes) of each token; the two 16-byte halves change places
-    // every four tokens, against bank conflicts
-    uint32_t o[8];
+  for (int c = 0; c < COLS / 32; ++c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 h = __float22bfloat162_rn(unpack_f32(acc[8 * c + i]));
-      o[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int p = 0; p < 4; ++p) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __float22bfloat162_rn(unpack_f32(acc[16 * c + 4 * p + i]));
+        o[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(piece(lane, p)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    uint8_t* mine = stg + lane * 32;
-    const int sw = (lane >> 2) & 1;
-    *reinterpret_cast<uint4*>(mine + 16 * sw) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(mine + 16 * (sw ^ 1)) = make_uint4(o[4], o[5], o[6], o[7]);
     __syncwarp();
-    const int n = n0 + 16 * c;
-    if (vec && n + 16 <= a.N) {
+    const int n = n0 + 32 * c;
+    if (vec && n + 32 <= a.N) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * i + (lane >> 1), p = lane & 1;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), p = lane & 3;
         if (m0 + r < mend)
           *reinterpret_cast<uint4*>(a.Y + (int64_t)(m0 + r) * a.ldy + n + 8 * p) =
-              *reinterpret_cast<const uint4*>(stg + r * 32 + 16 * (p ^ ((r >> 2) & 1)));
+              *reinterpret_cast<const uint4*>(piece(r, p));
       }
-    } else {
-      // rows at any address: two tokens at a time, a column per lane
-      const int k = lane & 15;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        if (m0 + r < mend && n + k < a.N)
-          a.Y[(int64_t)(m0 + r) * a.ldy + n + k] =
-              *reinterpret_cast<const uint16_t*>(stg + r * 32 + 16 * ((k >> 3) ^ ((r >> 2) & 1)) + 2 * (k & 7));
-      }
+    } else if (n + lane < a.N) {
+      // rows at any address: a token at a time, a column per lane
+      uint16_t* dst = a.Y + (int64_t)m0 * a.ldy + n + lane;
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r, dst += a.ldy)
+        if (m0 + r < mend) *dst = *reinterpret_cast<const uint16_t*>(piece(r, lane >> 3) + 2 * (lane & 7));
     }
     __syncwarp();
   }
@@ -608,7 +605,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
       } else {
-        store_rows<COLS>(a, acc, epi + warp * 1024, w.m0 + 32 * quarter, w.mend,
+        store_rows<COLS>(a, acc, epi + warp * 2048, w.m0 + 32 * quarter, w.mend,
                          w.n0 + col0, lane);
       }
     }
