@@ -127,11 +127,16 @@ def _device(*tensors) -> torch.device:
     return dev
 
 
+# the raw handle of a device's current stream, without making a Stream object of it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream, dev: torch.device) -> int:
     """The raw stream handle for a call on `dev`: the given stream (which must
     belong to `dev`) or that device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return _current_raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream

@@ -431,8 +431,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // block's MMAs.)
     const bool weights = warp == PW + 3;
     if (lane == 0) {
-      // with static weights theirs stream before the preceding work is done
-      if (!a.offsets && !(weights && a.static_weights)) asm volatile("griddepcontrol.wait;" ::: "memory");
+      // With static weights their first stages stream before the preceding work is
+      // done.  (Every bounded wait comes after the wait for that work, which may
+      // take any time.)
+      bool waited = a.offsets != nullptr;
+      if (!waited && !(weights && a.static_weights)) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      }
       const CUtensorMap* map = weights ? &tmap_w : &tmap_x;
       uint8_t* const dst0 = smem + (SWAP == weights ? 0 : kRows * kBlockK);  // operand A is first
       int st = 0, ph = 0, issued = 0;  // ph: parity that `empty` completes next
@@ -441,6 +447,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const Tile w = tile_of<C::TOK, C::WROWS>(t, a, pre, off);
         const int row = weights ? w.e * a.N + w.n0 : w.m0;
         for (int kb = kb0; kb < kb1; ++kb) {
+          if (issued == S && !waited) asm volatile("griddepcontrol.wait;" ::: "memory");
           if (issued >= S && !wait_or_fail(&bars->empty[st], ph, bars)) {
             ok = false;
             break;
@@ -492,6 +499,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // before every MMA)
     int st = 0, ph = 0, buf = 0, bph = 1;
     bool ok = true;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int t = first; t < tiles && ok; t += step) {
       for (int kb = kb0; kb < kb1; ++kb) {
         // (parity 1 passes at once on a fresh barrier: every buffer starts free)

@@ -449,6 +449,60 @@ def test_grouped_equals_dense(nv):
             check_product(Y[a:b], values(x[a:b], sx[a:b], 1), values(w[e], sw[e], 128), f"expert {e}")
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 300, 1024), (100, 700, 512), (900, 4100, 2048), (900, 4100, 2064)])
+def test_scales_at_any_4_byte_address(nv, M, N, K):
+    """Scales that start at odd multiples of 4 bytes, dense and grouped."""
+    x, w = whole_numbers((M, K), 1), whole_numbers((N, K), 2)
+    off = lambda t: torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)  # noqa: E731
+    sx, sw = powers((M, blocks(K)), 3), powers((blocks(N), blocks(K)), 4)
+    ref = (values(x, sx, 1) @ values(w, sw, 128).T).float().to(BF16)
+    ends = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    for a, b in ((off(sx), sw), (sx, off(sw)), (off(sx), off(sw))):
+        Y = torch.empty((M, N), dtype=BF16, device="cuda")
+        nv.fp8_gemm(x, a, w, b, Y)
+        assert torch.equal(Y, ref)
+        Y.fill_(0)
+        nv.fp8_gemm_grouped(x, a, w[None], b[None], ends, Y)
+        assert torch.equal(Y, ref)
+
+
+def test_elements_past_32_bits(nv):
+    """Tensors of more than 2^32 elements: the last rows are what a small call gives."""
+    M, K, n = 270000, 16384, 3
+    x = torch.zeros((M, K), dtype=BF16, device="cuda")
+    x[-n:] = randn((n, K), 1)
+    w = randn((K,), 2)
+    q, s = torch.empty((M, K), dtype=F8, device="cuda"), torch.empty((M, K // 128), dtype=F32, device="cuda")
+    nv.fp8_quantize(x, q, s)
+    q1, s1 = nv.fp8_quantize_new(x[-n:])
+    assert torch.equal(q[-n:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-n:], s1)
+    nv.fp8_rmsnorm(x, w, q=q, s=s)
+    nv.fp8_rmsnorm(x[-n:], w, q=q1, s=s1)
+    assert torch.equal(q[-n:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-n:], s1)
+    nv.fp8_quantize_weights(x, q, s[:blocks(M)])
+    q2, s2 = nv.fp8_quantize_weights_new(x[M // 128 * 128:])
+    assert torch.equal(q[M // 128 * 128:].view(torch.uint8), q2.view(torch.uint8))
+    assert torch.equal(s[blocks(M) - 1:blocks(M)], s2)
+    del x
+    # as activations, as weights of the last expert, and with a far row of Y
+    wq, sw = whole_numbers((130, K), 3), powers((2, K // 128), 4)
+    Y = torch.empty((M, 130), dtype=BF16, device="cuda")
+    nv.fp8_gemm(q, s, wq, sw, Y)
+    Y1 = torch.empty((M % 128, 130), dtype=BF16, device="cuda")
+    nv.fp8_gemm(q[M // 128 * 128:], s[M // 128 * 128:], wq, sw, Y1)
+    check_product(Y[M // 128 * 128:], values(q[M // 128 * 128:], s[M // 128 * 128:], 1), values(wq, sw, 128))
+    E, N = 100, 2700
+    xs, ss = whole_numbers((5, K), 5), powers((5, K // 128), 6)
+    we, se = q.view(E, N, K), powers((E, blocks(N), K // 128), 7)
+    we[E - 1] = whole_numbers((N, K), 8)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = 5
+    wide = torch.zeros((5, 1 << 30), dtype=BF16, device="cuda")
+    nv.fp8_gemm_grouped(xs, ss, we, se, offsets, wide[:, :N])
+    ref = (values(xs, ss, 1) @ values(we[E - 1], se[E - 1], 128).T).float().to(BF16)
+    assert torch.equal(wide[:, :N], ref)
+
+
 # ------------------------------------------------------------- empty, together
 
 def test_empty_calls(nv):
