@@ -537,19 +537,39 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
-def _ld(t: torch.Tensor | None) -> int:
-    """Leading dimension of a 2-D tensor; of a single row, whose stride says nothing, its length."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _first(t: torch.Tensor, dtype, what: str, ndim: int):
+    """Shape, device, address and leading dimension of the tensor that a call's
+    other tensors are checked against."""
+    _need(t, dtype, what, ndim)
+    shape = t.shape
+    # (the stride of a single row says nothing)
+    return shape, t.device, t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[-1]
 
 
-def _need_fp8(q: torch.Tensor, s: torch.Tensor, what: str, shape: tuple, scale_shape: tuple):
-    """q (checked to be a float8_e4m3fn CUDA tensor) of `shape` and its scales s
-    float32 of `scale_shape`, both contiguous."""
-    if not isinstance(s, torch.Tensor) or not s.is_cuda or s.dtype is not torch.float32:
-        _need(s, torch.float32, f"{what}'s scales")
-    if q.shape != shape or s.shape != scale_shape or not q.is_contiguous() or not s.is_contiguous():
-        raise ValueError(f"{what} must be contiguous {list(shape)} with scales {list(scale_shape)}, got "
-                         f"{tuple(q.shape)} and {tuple(s.shape)}")
+def _rows(t: torch.Tensor, dtype, what: str, shape, dev: torch.device):
+    """Address and leading dimension of 2-D `t` of the given shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index):
+        _need(t, dtype, what, 2)
+        raise ValueError(f"{what} is on {t.device}, not on {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1:
+        _need(t, dtype, what, 2)
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _dense(t: torch.Tensor, dtype, what: str, shape, dev: torch.device) -> int:
+    """Address of contiguous `t` of the given shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index):
+        _need(t, dtype, what)
+        raise ValueError(f"{what} is on {t.device}, not on {dev}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -559,54 +579,43 @@ def fp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     residual_out (default: residual itself, in place) receives bf16(x + residual),
     which is what is normed.  Outputs, at least one: y BF16 [M, K], and
     q float8_e4m3fn [M, K] with s float32 [M, ceil(K/128)]."""
-    _need(x, torch.bfloat16, "x", 2)
-    _need(weight, torch.bfloat16, "weight", 1)
-    shape = x.shape
+    shape, dev, px, ldx = _first(x, _BF16, "x", 2)
     M, K = shape
-    if weight.shape[0] != K:
-        raise ValueError(f"weight must hold K={K} elements, got {weight.shape[0]}")
-    if residual is None and residual_out is not None:
+    pw = _dense(weight, _BF16, "weight", (K,), dev)
+    pr = po = py = pq = ps = None
+    ldr = ldo = ldy = 0
+    if residual is not None:
+        pr, ldr = _rows(residual, _BF16, "residual", shape, dev)
+        po, ldo = (pr, ldr) if residual_out is None else _rows(residual_out, _BF16, "residual_out", shape, dev)
+    elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if residual is not None and residual_out is None:
-        residual_out = residual
-    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
-        if t is not None:
-            _need(t, torch.bfloat16, what, 2)
-            if t.shape != shape:
-                raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if y is not None:
+        py, ldy = _rows(y, _BF16, "y", shape, dev)
     if (q is None) != (s is None):
         raise ValueError("q and s go together")
     if q is not None:
-        _need(q, _F8, "q", 2)
-        _need_fp8(q, s, "q", shape, (M, _blocks(K)))
-    dev = _device(x, weight, residual, residual_out, y, q, s)
-    _call("fp8_rmsnorm", dev, _ptr(x), _ld(x), _ptr(weight), _ptr(residual), _ld(residual), _ptr(residual_out),
-          _ld(residual_out), _ptr(y), _ld(y), _ptr(q), _ptr(s), M, K, float(eps), _stream(stream, dev))
+        pq = _dense(q, _F8, "q", shape, dev)
+        ps = _dense(s, _F32, "s", (M, (K + 127) // 128), dev)
+    _call("fp8_rmsnorm", dev, px, ldx, pw, pr, ldr, po, ldo, py, ldy, pq, ps, M, K, eps, _stream(stream, dev))
 
 
 def fp8_quantize(X: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gated: bool = False, stream=None) -> None:
     """BF16 activations X [M, K] into q float8_e4m3fn [M, K] and s float32 [M, ceil(K/128)].
     gated: X is [M, 2K], gate then up columns, and silu(gate) * up is quantized."""
-    _need(X, torch.bfloat16, "X", 2)
-    M, cols = X.shape
-    if gated and cols % 2:
-        raise ValueError(f"a gated X has an even number of columns, got {cols}")
-    K = cols // 2 if gated else cols
-    _need(q, _F8, "q", 2)
-    _need_fp8(q, s, "q", (M, K), (M, _blocks(K)))
-    dev = _device(X, q, s)
-    _call("fp8_quantize", dev, _ptr(X), _ld(X), M, K, _ptr(q), _ptr(s), FLAG_FP8_GATED if gated else 0,
-          _stream(stream, dev))
+    (M, K), dev, px, ldx = _first(X, _BF16, "X", 2)
+    if gated:
+        if K % 2:
+            raise ValueError(f"a gated X has an even number of columns, got {K}")
+        K //= 2
+    _call("fp8_quantize", dev, px, ldx, M, K, _dense(q, _F8, "q", (M, K), dev),
+          _dense(s, _F32, "s", (M, (K + 127) // 128), dev), FLAG_FP8_GATED if gated else 0, _stream(stream, dev))
 
 
 def fp8_quantize_weights(W: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
     """BF16 weights W [N, K] into q float8_e4m3fn [N, K] and s float32 [ceil(N/128), ceil(K/128)]."""
-    _need(W, torch.bfloat16, "W", 2)
-    N, K = W.shape
-    _need(q, _F8, "q", 2)
-    _need_fp8(q, s, "q", (N, K), (_blocks(N), _blocks(K)))
-    dev = _device(W, q, s)
-    _call("fp8_quantize_weights", dev, _ptr(W), _ld(W), N, K, _ptr(q), _ptr(s), _stream(stream, dev))
+    (N, K), dev, pw, ldw = _first(W, _BF16, "W", 2)
+    _call("fp8_quantize_weights", dev, pw, ldw, N, K, _dense(q, _F8, "q", (N, K), dev),
+          _dense(s, _F32, "s", (_blocks(N), _blocks(K)), dev), _stream(stream, dev))
 
 
 def fp8_gemm(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, Y: torch.Tensor, stream=None,
@@ -615,16 +624,12 @@ def fp8_gemm(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: torch.Tenso
     (fp8_quantize, fp8_rmsnorm), weights w [N, K], sw [ceil(N/128), ceil(K/128)]
     (fp8_quantize_weights).  static_weights: w is not written by work still
     running on the stream (NVFP4_FLAG_STATIC_WEIGHTS)."""
-    _need(x, _F8, "x", 2)
+    (M, K), dev, _, _ = _first(x, _F8, "x", 2)
     _need(w, _F8, "w", 2)
-    _need(Y, torch.bfloat16, "Y", 2)
-    (M, K), N = x.shape, w.shape[0]
-    _need_fp8(x, sx, "x", (M, K), (M, _blocks(K)))
-    _need_fp8(w, sw, "w", (N, K), (_blocks(N), _blocks(K)))
-    if Y.shape != (M, N):
-        raise ValueError(f"Y must be {(M, N)}, got {tuple(Y.shape)}")
-    dev = _device(x, sx, w, sw, Y)
-    _call("fp8_gemm", dev, _ptr(x), _ptr(sx), _ptr(w), _ptr(sw), _ptr(Y), _ld(Y), M, N, K,
+    N, kb = w.shape[0], (K + 127) // 128
+    py, ldy = _rows(Y, _BF16, "Y", (M, N), dev)
+    _call("fp8_gemm", dev, _dense(x, _F8, "x", (M, K), dev), _dense(sx, _F32, "sx", (M, kb), dev),
+          _dense(w, _F8, "w", (N, K), dev), _dense(sw, _F32, "sw", ((N + 127) // 128, kb), dev), py, ldy, M, N, K,
           FLAG_STATIC_WEIGHTS if static_weights else 0, _stream(stream, dev))
 
 
@@ -634,18 +639,14 @@ def fp8_gemm_grouped(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: tor
     belong to expert e of w [E, N, K], sw [E, ceil(N/128), ceil(K/128)].  offsets:
     int32 [E + 1] on the device, not decreasing.  Rows of Y outside
     offsets[0] .. offsets[E]-1 keep what they hold."""
+    (E, N, K), dev, _, _ = _first(w, _F8, "w", 3)
     _need(x, _F8, "x", 2)
-    _need(w, _F8, "w", 3)
-    _need(offsets, torch.int32, "offsets", 1)
-    _need(Y, torch.bfloat16, "Y", 2)
-    (T, K), (E, N) = x.shape, w.shape[:2]
-    _need_fp8(x, sx, "x", (T, K), (T, _blocks(K)))
-    _need_fp8(w, sw, "w", (E, N, K), (E, _blocks(N), _blocks(K)))
-    if Y.shape != (T, N) or offsets.shape[0] != E + 1:
-        raise ValueError(f"Y must be {(T, N)} and offsets hold {E + 1}, got {tuple(Y.shape)} and {offsets.shape[0]}")
-    dev = _device(x, sx, w, sw, offsets, Y)
-    _call("fp8_gemm_grouped", dev, _ptr(x), _ptr(sx), _ptr(w), _ptr(sw), _ptr(offsets), _ptr(Y), _ld(Y), T, E, N,
-          K, FLAG_STATIC_WEIGHTS if static_weights else 0, _stream(stream, dev))
+    T, kb = x.shape[0], (K + 127) // 128
+    py, ldy = _rows(Y, _BF16, "Y", (T, N), dev)
+    _call("fp8_gemm_grouped", dev, _dense(x, _F8, "x", (T, K), dev), _dense(sx, _F32, "sx", (T, kb), dev),
+          _dense(w, _F8, "w", (E, N, K), dev), _dense(sw, _F32, "sw", (E, (N + 127) // 128, kb), dev),
+          _dense(offsets, torch.int32, "offsets", (E + 1,), dev), py, ldy, T, E, N, K,
+          FLAG_STATIC_WEIGHTS if static_weights else 0, _stream(stream, dev))
 
 
 def fp8_quantize_new(X: torch.Tensor, gated: bool = False, stream=None):
