@@ -16,12 +16,21 @@
 //   !SWAP the rows are tokens, the BN = 256 columns weight rows.  A thread owns
 //         128 columns of one token, so its scale is one product per block.  For
 //         many tokens.
-// Roles per CTA: PW promotion warps, one producer warp (lane 0 issues the TMA
-// tiles; all lanes copy the block's scales with cp.async into a ring of their
-// own), one MMA warp.  Persistent over tiles; the stage ring runs on across
-// tiles.  With few tiles a cluster of `splits` CTAs shares a tile's blocks of k
-// and adds the partial sums in rank order through distributed shared memory.
-// Every wait is bounded.
+// Roles per CTA: PW promotion warps; two producer threads (TMA tiles of the tokens
+// and of the weights); one MMA warp; SWAP: a warp that copies the block's scales
+// into a ring of slots with cp.async.  Persistent over tiles; the stage ring runs
+// on across tiles.  With few tiles a cluster of `splits` CTAs shares a tile's
+// blocks of k and adds the partial sums in rank order through distributed shared
+// memory.  Every wait is bounded.
+//
+// What bounds it (one B200): few tokens, the weight stream (one token through
+// 17408 x 5120: 17.0 us, 81% of the copy rate); many, the power limit (4096 tokens
+// through 17408 x 5120: 298 us or 2.45 PFLOP/s in a burst, 362 us at 1.5 GHz in a
+// loop) and L2 to SM: bulk copies alone reach 58 bytes per cycle and SM, so a
+// 128 x 256 x 128 block's 48 KB take 847 cycles against 512 of MMAs, and a block
+// takes 850 to 880.  Pairs of SMs with 256 x 256 tiles, which load a third less,
+// ran at 330 us: the chain commit, promotion, arrival at the other SM, next MMA is
+// longer than two accumulators cover.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -748,8 +757,8 @@ struct Problem {
   // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
   // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
   // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
-  // 0.8 and 0.025 per token of the tile.  The choices by this rule run within 15%
-  // of the best one of each shape there, mostly within 5%; by tile width alone
+  // 0.8 and 0.025 per token of the tile.  The choices by this rule run within 7%
+  // of the best one of each shape there but for one (19%); by tile width alone
   // (M <= 16: 16 tokens, and so on) they were up to 2.7 times slower.
   template <class C>
   double estimate(int c) const {

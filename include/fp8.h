@@ -5,11 +5,11 @@
  * asynchronous on `stream`, host-side validation, nothing allocated, no
  * synchronization).
  *
- * The quantization pages list FP8 weights beside NVFP4 ones (block-FP8 layers
- * of the model card "Qwen3.8-27B-NVFP4", vLLM paragraph); they give no kernels.
- * Here an 8-bit layer is four calls: the RMS norm (or the gated activation)
- * writes 8-bit activations, and the product, dense or grouped by expert,
- * multiplies them by 8-bit weights.
+ * The pages name block-FP8 weights only as the format that another engine falls
+ * back to (model card "Qwen3.8-27B-NVFP4", vLLM paragraph) and give no kernels.
+ * Here an 8-bit layer is four kinds of call: the RMS norm or a quantizer writes
+ * 8-bit activations, and the product, dense or grouped by expert, multiplies
+ * them by 8-bit weights.
  *
  * Layouts (row-major, no padding inside a row; kb = ceil(K / 128); the last
  * block of a row or column may be short):
