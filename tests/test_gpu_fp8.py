@@ -307,6 +307,36 @@ def test_gemm_whole_numbers_are_exact(nv, M, N, K):
     chk()
 
 
+@pytest.mark.parametrize("M,N,K", [(200, 130, 2064), (90, 1001, 2064), (90, 2560, 5120), (90, 5125, 5120),
+                                   (128, 1001, 5120), (64, 5125, 2064), (90, 17408, 528), (130, 5125, 5120),
+                                   (128, 5125, 2064), (130, 2560, 5120), (384, 1001, 5120), (128, 17411, 2064),
+                                   (256, 5120, 2064), (100, 5125, 17408), (250, 5120, 17408)])
+def test_gemm_every_tile_width_and_split(nv, M, N, K):
+    """Middle sizes, where every tile width and split of k is chosen for some."""
+    x, w = whole_numbers((M, K), M + K), whole_numbers((N, K), N + K)
+    sx, sw = powers((M, blocks(K)), M), powers((blocks(N), blocks(K)), N)
+    Y, chk = guarded_empty((M, N), BF16)
+    nv.fp8_gemm(x, sx, w, sw, Y)
+    assert torch.equal(Y, (values(x, sx, 1) @ values(w, sw, 128).T).float().to(BF16))
+    chk()
+
+
+@pytest.mark.parametrize("T,E,N,K", [(1000, 8, 1536, 1040), (900, 4, 1540, 1040), (2000, 20, 1536, 144),
+                                     (900, 4, 1536, 4112), (2000, 20, 1001, 144), (700, 5, 1001, 1040)])
+def test_grouped_every_tile_width(nv, T, E, N, K):
+    g = torch.Generator().manual_seed(T + E)
+    ends = [0, *sorted(torch.randint(0, T + 1, (E - 1,), generator=g).tolist()), T - 3]
+    ends = [min(e, T - 3) for e in ends]
+    x, w = whole_numbers((T, K), 1), whole_numbers((E, N, K), 2)
+    sx, sw = powers((T, blocks(K)), 3), powers((E, blocks(N), blocks(K)), 4)
+    Y, chk = guarded_empty((T, N), BF16)
+    Y.fill_(5.0)
+    ref = grouped_ref(x, sx, w, sw, ends, Y)
+    nv.fp8_gemm_grouped(x, sx, w, sw, torch.tensor(ends, dtype=torch.int32, device="cuda"), Y)
+    assert torch.equal(Y, ref)
+    chk()
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 1001, 5120), (20, 5120, 2064), (60, 300, 17408), (100, 700, 4096),
                                    (520, 17408, 1040), (1111, 4097, 2048)])
 def test_gemm_random(nv, M, N, K):
