@@ -9,10 +9,10 @@
 // fmaxf drops NaN, so a NaN element stays a NaN code of its own and leaves the
 // rest of its block alone; an infinity makes its block's scale infinite.
 //
-// All three stream HBM once.  A thread owns 16-byte vectors (8 columns) that
-// are consecutive across lanes, so a block of 128 columns is 16 neighbouring
-// lanes and its maximum takes four shuffles; K is a multiple of 16, so no
-// vector straddles the end of a row.
+// All three stream HBM once.  A thread owns 16-byte vectors (8 columns; the
+// activation quantizer's 16) that are consecutive across lanes, so a block of 128
+// columns is 16 (8) neighbouring lanes and its maximum takes four (three)
+// shuffles; K is a multiple of 16, so no lane straddles the end of a row.
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -318,41 +318,49 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fmul_rn(__fdividef(g, 1.0f + __expf(-g)), u);
 }
 
-// Activation quantizer: 16 lanes per block of 128 columns, one block per 16
-// lanes and step at full occupancy.  (4096 x 5120: 14.7 us, 67% of the copy rate
-// with about 1.5 us of launch; with two or four blocks of a lane in flight and
-// as many fewer warps 14.9 to 18.9 us.)
+// Activation quantizer: 8 lanes of 16 columns per block of 128, two (gated: four)
+// 16-byte loads of a lane in flight at six CTAs per SM.  4096 x 5120: 12.4 us, 80%
+// of the copy rate; gated 1024 x 17408: 17.5 us, 80%.  (16 lanes of 8 columns at
+// eight CTAs: 14.6 and 20.2 us; two or four blocks of a lane in flight with as many
+// fewer warps: 14.9 to 18.9 us.)
 template <bool GATED>
-__global__ void __launch_bounds__(256, 8) quantize_rows_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(256, 6) quantize_rows_kernel(const QuantArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane16 = threadIdx.x & 15;
-  const uint64_t stride = (uint64_t)gridDim.x * 16;
-  // (whole warps stay in the loop: both halves of a warp take part in the shuffles)
-  for (uint64_t b = (uint64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; b < a.blocks; b += stride) {
-    const uint32_t blk = (uint32_t)b + ((threadIdx.x >> 4) & 1);
+  const int lane8 = threadIdx.x & 7;
+  const uint64_t stride = (uint64_t)gridDim.x * 32;
+  // (whole warps stay in the loop: all four blocks of a warp take part in the shuffles)
+  for (uint64_t b = (uint64_t)blockIdx.x * 32 + (threadIdx.x >> 5) * 4; b < a.blocks; b += stride) {
+    const uint32_t blk = (uint32_t)b + ((threadIdx.x >> 3) & 3);
     const uint32_t row = blk / (uint32_t)a.kb;
-    const int c = (int)(blk - row * (uint32_t)a.kb) * 128 + lane16 * 8;
-    const bool in = blk < a.blocks && c < a.K;
-    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int c = (int)(blk - row * (uint32_t)a.kb) * 128 + lane8 * 16;
+    const bool in = blk < a.blocks && c < a.K;  // K is a multiple of 16: all 16 columns or none
+    float f[2][8] = {};
     if (in) {
       const uint16_t* p = a.x + (int64_t)row * a.ldx + c;
-      const uint4 v = ld_stream_v4(p);
+      const uint4 v0 = ld_stream_v4(p), v1 = ld_stream_v4(p + 8);
+      unpack8(v0, f[0]);
+      unpack8(v1, f[1]);
       if (GATED) {
-        const uint4 u = ld_stream_v4(p + a.K);
+        const uint4 u0 = ld_stream_v4(p + a.K), u1 = ld_stream_v4(p + a.K + 8);
         float uf[8];
-        unpack8(v, f);
-        unpack8(u, uf);
+        unpack8(u0, uf);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = silu_mul(f[i], uf[i]);
-      } else {
-        unpack8(v, f);
+        for (int i = 0; i < 8; ++i) f[0][i] = silu_mul(f[0][i], uf[i]);
+        unpack8(u1, uf);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[1][i] = silu_mul(f[1][i], uf[i]);
       }
     }
-    const float s = scale_of(max16(absmax(f)));
+    float m = fmaxf(absmax(f[0]), absmax(f[1]));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float s = scale_of(m);
     if (in) {
-      *reinterpret_cast<uint2*>(a.q + (int64_t)row * a.K + c) = quantize8(f, __frcp_rn(s));
-      if (lane16 == 0) a.s[blk] = s;
+      const float r = __frcp_rn(s);
+      const uint2 lo = quantize8(f[0], r), hi = quantize8(f[1], r);
+      *reinterpret_cast<uint4*>(a.q + (int64_t)row * a.K + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if (lane8 == 0) a.s[blk] = s;
     }
   }
 }
@@ -450,7 +458,7 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, int64_t ldx, int64_t M, int64
                                 int sms, cudaStream_t stream) {
   const int64_t kb = (K + 127) / 128;
   QuantArgs a{x, q, s, ldx, (uint32_t)(M * kb), (int)K, (int)kb};
-  const int64_t want = (M * kb + 15) / 16, most = (int64_t)sms * 8;
+  const int64_t want = (M * kb + 31) / 32, most = (int64_t)sms * 6;
   void* args[] = {&a};
   return tc::launch_pdl(gated ? (const void*)quantize_rows_kernel<true> : (const void*)quantize_rows_kernel<false>,
                         dim3((unsigned)(want < most ? want : most)), dim3(256), 0, stream, args);
