@@ -179,9 +179,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int thr
 
 // Many rows: each CTA takes rows blockIdx.x, + gridDim.x, ... and bulk copies
 // bring them into a ring of row slots (x, then the residual) ahead of time, so
-// that reads go on while a row is summed, scaled and stored.  8192 rows of 5120
-// with a residual: 295 MB; a CTA per row, its loads waiting for its place on the
-// SM, took 73.6 us (62% of the copy rate).
+// that reads go on while a row is summed, scaled and stored.  A thread has VPT
+// neighbouring vectors, so a block of 128 columns is 16 / VPT lanes.  8192 rows of
+// 5120 with a residual (295 MB): 51.7 us, 88% of the copy rate; a CTA per row, its
+// loads waiting for its place on the SM, 73.6 us.  Without the residual the
+// arithmetic per byte bounds it (8192 x 5120: 38 us, 52%).
 template <int VPT>
 __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, int slots) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
   uint4 wv[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (t + i * threads) * 8;
+    const int c = (t * VPT + i) * 8;
     wv[i] = c < a.K ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
   }
   int slot = 0, ph = 0, odd = 0;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
     float f[VPT][8], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * threads) * 8;
+      const int c = (t * VPT + i) * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
       if (c < a.K) {
@@ -254,10 +256,37 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
     }
     sum = warp_sum((t & 31) < (threads >> 5) ? red[odd][t & 31] : 0.0f);
     const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.K), a.eps));
+    float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * threads) * 8;
-      norm_out(a, row, c, c < a.K, f[i], wv[i], rstd);
+      float w[8];
+      unpack8(wv[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = __fmul_rn(__fmul_rn(f[i][j], rstd), w[j]);
+      m = fmaxf(m, absmax(f[i]));
+    }
+    if (a.q) {  // the block's other columns are with the next 16 / VPT - 1 lanes
+#pragma unroll
+      for (int o = 8 / VPT; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    }
+    const float s = scale_of(m), r = __frcp_rn(s);
+    const int c0 = t * VPT * 8;
+    if (c0 < a.K) {
+#pragma unroll
+      for (int i = 0; i < VPT; i += 2) {  // K is a multiple of 16: pairs of vectors are in or out together
+        const int c = c0 + i * 8;
+        if (c < a.K) {
+          if (a.y) {
+            *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = pack8(f[i]);
+            *reinterpret_cast<uint4*>(a.y + row * a.ldy + c + 8) = pack8(f[i + 1]);
+          }
+          if (a.q) {
+            const uint2 lo = quantize8(f[i], r), hi = quantize8(f[i + 1], r);
+            *reinterpret_cast<uint4*>(a.q + row * a.K + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          }
+        }
+      }
+      if (a.q && (c0 & 127) == 0) a.s[row * a.kb + (c0 >> 7)] = s;
     }
     odd ^= 1;
     if (++slot == slots) slot = 0, ph ^= 1;
@@ -428,23 +457,26 @@ cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* w
     threads = (int)(((vecs + vpt - 1) / vpt + 31) / 32 * 32);
   }
   if (threads > 32 && M > 2 * (int64_t)sms) {
-    // as many CTAs per SM as hold its 2048 threads and at least two rows each
+    // about 20 warps per SM with a residual and 30 without (fewer bytes, more
+    // arithmetic per byte; measured from 2 to 6 CTAs at K = 1040 to 16384), and at
+    // least two CTAs with at least two rows each where the SM holds them
+    const int wide = vecs <= 2048 ? 2 : 4, group = (int)((vecs + wide - 1) / wide + 31) / 32 * 32;
     const int slot = (int)K * (residual ? 4 : 2);
-    int per_sm = 2048 / threads < 3 ? 2048 / threads : 3, slots = 0;
+    int per_sm = (residual ? 20 : 30) * 32 / group, slots = 0;
+    if (per_sm < 2 && 2 * group <= 2048) per_sm = 2;
     for (; per_sm > 0; --per_sm) {
       slots = (kNormSmem / per_sm - 2048) / slot;
       if (slots >= 2) break;
     }
     if (slots > kNormSlots) slots = kNormSlots;
     if (per_sm > 0) {
-      static tc::SmemOptIn opt[3];
-      const void* fn = vpt == 1 ? (const void*)rmsnorm_rows_kernel<1> : vpt == 2 ? (const void*)rmsnorm_rows_kernel<2>
-                                                                                : (const void*)rmsnorm_rows_kernel<4>;
-      cudaError_t e = opt[vpt >> 1].ensure(fn, slots * slot);
+      static tc::SmemOptIn opt[2];
+      const void* fn = wide == 2 ? (const void*)rmsnorm_rows_kernel<2> : (const void*)rmsnorm_rows_kernel<4>;
+      cudaError_t e = opt[wide == 4].ensure(fn, slots * slot);
       if (e != cudaSuccess) return e;
       const int64_t grid = (int64_t)sms * per_sm;
       void* args[] = {&a, &slots};
-      return tc::launch_pdl(fn, dim3((unsigned)(M < grid ? M : grid)), dim3(threads), slots * slot, stream, args);
+      return tc::launch_pdl(fn, dim3((unsigned)(M < grid ? M : grid)), dim3(group), slots * slot, stream, args);
     }
   }
   const int rows = threads == 32 ? 4 : 1;
