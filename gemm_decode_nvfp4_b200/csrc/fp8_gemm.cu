@@ -93,9 +93,9 @@ struct Cfg {
   static constexpr uint32_t TMEM = NBUF * BN < 32 ? 32 : NBUF * BN;
   static constexpr int COLS = BN / (PW / 4);  // accumulator columns of one thread
   static constexpr int TOK = SWAP ? BN : kRows, WROWS = SWAP ? kRows : BN;
-  static constexpr int LD = SWAP ? 16 : 32;
-  static constexpr int LDBUF = 2;  // 32-column register buffers of a promotion warp
-  static constexpr int SLOT = TOK + 4;        // floats of a scale slot: token scales, then the weight scale
+  static constexpr int LD = SWAP ? 16 : 32;  // columns of a tensor-memory load (of 16 at a time) ...
+  static constexpr int LDBUF = 2;            // ... and the register buffers for them
+  static constexpr int SLOT = TOK + 4;       // floats of a scale slot: token scales, then the weight scale
   static constexpr int STAGE = (kRows + BN) * kBlockK;
   static constexpr int THREADS = (PW + 4) * 32;
   static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
@@ -104,7 +104,8 @@ struct Cfg {
   static constexpr int FIXED = EPI + SCALES + (int)sizeof(Bars) + 1024;
 };
 
-// The same by one thread.
+// Wait for the phase with the given parity, kWaitClocks at most; then the CTA's
+// error is recorded and its other waits fail too.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Bars* bars) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
@@ -127,7 +128,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The warp waits for the phase (all lanes poll: one lane's tries took longer);
+// The warp waits for the phase (all lanes poll; with one lane's tries the products
+// took 10 to 15% longer);
 // the vote makes the answer the warp's, so that code after it stays convergent.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars) {
   const bool ok = __all_sync(0xFFFFFFFFu, wait_or_fail(bar, parity, bars));
