@@ -142,6 +142,23 @@ def _stream(stream, dev: torch.device) -> int:
     return stream.cuda_stream
 
 
+def _on_stream(stream, dev: torch.device, fn, *args, **kw):
+    """fn(*args, **kw) with `stream` current, for the functions that allocate: what
+    they allocate and copy then belongs to the stream that their kernels run on.
+    (Memory of the current stream could still be in use by its earlier work, and
+    a temporary of it would be handed on while `stream` reads it.)  The caller may
+    use the returned tensors on the current stream, ordered after `stream`, and drop
+    them there."""
+    if dev.type == "cuda":
+        _stream(stream, dev)
+    with torch.cuda.stream(stream):
+        out = fn(*args, **kw)
+    if dev.type == "cuda":
+        for t in out if isinstance(out, tuple) else (out,):
+            t.record_stream(torch.cuda.current_stream(dev))
+    return out
+
+
 def _call(fn: str, dev: torch.device, *args) -> None:
     """Call lib.<fn>(*args) with `dev` current (the library launches on the
     current device) and raise on a non-zero status."""
@@ -651,26 +668,32 @@ def fp8_gemm_grouped(x: torch.Tensor, sx: torch.Tensor, w: torch.Tensor, sw: tor
 
 def fp8_quantize_new(X: torch.Tensor, gated: bool = False, stream=None):
     """Allocate q, s on X's device and quantize activations into them."""
+    if stream is not None:
+        return _on_stream(stream, X.device, fp8_quantize_new, X, gated=gated)
     M, K = X.shape[0], X.shape[1] // 2 if gated else X.shape[1]
     q = torch.empty((M, K), dtype=_F8, device=X.device)
     s = torch.empty((M, _blocks(K)), dtype=torch.float32, device=X.device)
-    fp8_quantize(X, q, s, gated=gated, stream=stream)
+    fp8_quantize(X, q, s, gated=gated)
     return q, s
 
 
 def fp8_quantize_weights_new(W: torch.Tensor, stream=None):
     """Allocate q, s on W's device and quantize weights into them."""
+    if stream is not None:
+        return _on_stream(stream, W.device, fp8_quantize_weights_new, W)
     N, K = W.shape
     q = torch.empty((N, K), dtype=_F8, device=W.device)
     s = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
-    fp8_quantize_weights(W, q, s, stream=stream)
+    fp8_quantize_weights(W, q, s)
     return q, s
 
 
 def fp8_linear(X: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, stream=None) -> torch.Tensor:
     """Quantize BF16 X [M, K] and multiply by 8-bit weights: allocates and returns Y [M, N]."""
+    if stream is not None:
+        return _on_stream(stream, X.device, fp8_linear, X, w, sw)
     X2 = X if X.dim() == 2 else X.reshape(1, -1)
-    q, s = fp8_quantize_new(X2, stream=stream)
+    q, s = fp8_quantize_new(X2)
     Y = torch.empty((X2.shape[0], w.shape[0]), dtype=torch.bfloat16, device=X.device)
-    fp8_gemm(q, s, w, sw, Y, stream=stream)
+    fp8_gemm(q, s, w, sw, Y)
     return Y if X.dim() == 2 else Y.reshape(-1)
