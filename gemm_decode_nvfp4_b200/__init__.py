@@ -153,7 +153,7 @@ def _on_stream(stream, dev: torch.device, fn, *args, **kw):
         _stream(stream, dev)
     with torch.cuda.stream(stream):
         out = fn(*args, **kw)
-    if dev.type == "cuda":
+    if dev.type == "cuda" and out is not None:
         for t in out if isinstance(out, tuple) else (out,):
             t.record_stream(torch.cuda.current_stream(dev))
     return out
@@ -193,8 +193,10 @@ def amax(w: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """out = max(out, max|w|) for a BF16 matrix w (out: float32 [1] on the device)."""
     _need(w, torch.bfloat16, "w")
     _need(out, torch.float32, "out")
-    w2 = w if w.dim() == 2 else w.reshape(1, -1)
     dev = _device(w, out)
+    if w.dim() != 2 and stream is not None:   # (reshape may copy)
+        return _on_stream(stream, dev, amax, w, out)
+    w2 = w if w.dim() == 2 else w.reshape(1, -1)
     _call("nvfp4_amax", dev, _ptr(w2), w2.shape[0], w2.shape[1], w2.stride(0), _ptr(out), _stream(stream, dev))
 
 
@@ -334,21 +336,25 @@ def gemm_noalloc(X: torch.Tensor, q: torch.Tensor, s: torch.Tensor, g: torch.Ten
 
 def quantize_new(w: torch.Tensor, amax: torch.Tensor | None = None, stream=None):
     """Allocate q, s, g on w's device and quantize into them."""
+    if stream is not None:
+        return _on_stream(stream, w.device, quantize_new, w, amax=amax)
     N, K = w.shape
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     s = torch.empty((N, K // 16), dtype=torch.uint8, device=w.device)
     g = torch.empty((1,), dtype=torch.float32, device=w.device)
-    quantize(w, q, s, g, amax=amax, stream=stream)
+    quantize(w, q, s, g, amax=amax)
     return q, s, g
 
 
 def linear(X: torch.Tensor, q: torch.Tensor, s: torch.Tensor, g: torch.Tensor, stream=None) -> torch.Tensor:
     """Allocate Y and run the GEMM (the GEMV when X has one row)."""
+    if stream is not None:
+        return _on_stream(stream, X.device, linear, X, q, s, g)
     X2 = X if X.dim() == 2 else X.reshape(1, -1)
     Y = torch.empty((X2.shape[0], q.shape[0]), dtype=torch.bfloat16, device=X.device)
     n_ws = gemm_workspace_size(X2.shape[0], q.shape[0], X2.shape[1])
     ws = torch.empty((n_ws,), dtype=torch.uint8, device=X.device) if n_ws else None
-    gemm(X2, q, s, g, Y, workspace=ws, stream=stream)
+    gemm(X2, q, s, g, Y, workspace=ws)
     return Y if X.dim() == 2 else Y.reshape(-1)
 
 
@@ -372,10 +378,12 @@ def mx_quantize(w: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) 
 
 def mx_quantize_new(w: torch.Tensor, stream=None):
     """Allocate q, s on w's device and MXFP4-quantize into them."""
+    if stream is not None:
+        return _on_stream(stream, w.device, mx_quantize_new, w)
     N, K = w.shape
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     s = torch.empty((N, K // 32), dtype=torch.uint8, device=w.device)
-    mx_quantize(w, q, s, stream=stream)
+    mx_quantize(w, q, s)
     return q, s
 
 
@@ -433,9 +441,11 @@ def mx_to_nvfp4(q: torch.Tensor, s_mx: torch.Tensor, stream=None):
     N, K = q.shape[0], q.shape[1] * 2
     if not q.is_contiguous() or not s_mx.is_contiguous() or s_mx.shape != (N, K // 32):
         raise ValueError("q/s_mx must be contiguous [N, K/2] / [N, K/32]")
+    dev = _device(q, s_mx)
+    if stream is not None:
+        return _on_stream(stream, dev, mx_to_nvfp4, q, s_mx)
     s_nv = torch.empty((N, K // 16), dtype=torch.uint8, device=q.device)
     g = torch.empty((1,), dtype=torch.float32, device=q.device)
-    dev = _device(q, s_mx)
     _call("mxfp4_to_nvfp4_scales", dev, _ptr(q), _ptr(s_mx), N, K, _ptr(s_nv), _ptr(g), _stream(stream, dev))
     return s_nv, g
 
@@ -454,8 +464,10 @@ def w4a4_prepare_weights(s: torch.Tensor, K: int, stream=None) -> torch.Tensor:
     N = s.shape[0]
     if not s.is_contiguous() or s.shape[1] * 16 != K:
         raise ValueError("s must be contiguous [N, K/16]")
-    out = torch.empty((lib.nvfp4_w4a4_weight_scales_bytes(N, K),), dtype=torch.uint8, device=s.device)
     dev = _device(s)
+    if stream is not None:
+        return _on_stream(stream, dev, w4a4_prepare_weights, s, K)
+    out = torch.empty((lib.nvfp4_w4a4_weight_scales_bytes(N, K),), dtype=torch.uint8, device=s.device)
     _call("nvfp4_w4a4_prepare_weights", dev, _ptr(s), N, K, _ptr(out), _stream(stream, dev))
     return out
 
@@ -472,9 +484,11 @@ def w4a4_quantize_x(X: torch.Tensor, x_amax: torch.Tensor, given_amax: bool = Fa
     if X.stride(1) != 1:
         raise ValueError("X rows must be contiguous")
     ldx = X.stride(0)
+    dev = _device(X, x_amax)
+    if stream is not None:
+        return _on_stream(stream, dev, w4a4_quantize_x, X, x_amax, given_amax=given_amax)
     qx = torch.empty((M, K // 2), dtype=torch.uint8, device=X.device)
     sx = torch.empty((lib.nvfp4_w4a4_x_scales_bytes(M, K),), dtype=torch.uint8, device=X.device)
-    dev = _device(X, x_amax)
     _call("nvfp4_w4a4_quantize_x", dev, _ptr(X), ldx, M, K, _ptr(qx), _ptr(sx), _ptr(x_amax),
           GIVEN_AMAX if given_amax else 0, _stream(stream, dev))
     return qx, sx
