@@ -35,6 +35,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include "fp8_drain.h"
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -77,6 +78,7 @@ struct Bars {
   uint64_t mma_done;
   uint32_t tmem_addr;
   volatile int err;
+  int issued[2];  // loads of the tokens' and the weights' tiles, when their producers are done
 };
 
 // !SWAP: 168 registers a thread (384 threads) do not hold 128 accumulators and
@@ -364,6 +366,21 @@ __device__ __forceinline__ void store_rows(const Args& a, const uint64_t (&acc)[
   }
 }
 
+// The loads that a CTA which gave up still has in flight.  (Out of line and at the end
+// of the kernel: elsewhere it changed the main loop's registers, 3% of some calls.)
+template <class C>
+__device__ __noinline__ void drain(Bars* bars, int stages, const CUtensorMap* tmap_w, uint8_t* dst_w) {
+  struct Ops {
+    Bars* bars;
+    const CUtensorMap* tmap_w;
+    uint8_t* dst_w;
+    __device__ void arm_b(int st) { ptx::mbar_arrive_expect_tx(&bars->full[st], C::WROWS * kBlockK); }
+    __device__ void load_b(int st) { ptx::tma_load_2d(dst_w + st * C::STAGE, tmap_w, &bars->full[st], 0, 0); }
+    __device__ void wait(int st, int parity) { ptx::mbar_wait(&bars->full[st], parity, kDrainNs); }
+  };
+  drain_ring(bars->issued[0], bars->issued[1], stages, Ops{bars, tmap_w, dst_w});
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -505,10 +522,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
       }
-      if (bars->err && !weights) {
-        // let the tiles already asked for land before the CTA exits
-        for (int g = max(issued - S, 0); g < issued; ++g) ptx::mbar_wait(&bars->full[g % S], (g / S) & 1, kDrainNs);
-      }
+      bars->issued[weights] = issued;
     }
     __syncwarp();
    } else if (SWAP && warp == PW + 2) {
@@ -712,6 +726,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       ptx::cluster_sync();
     }
   }
+  // (every role has stopped: no load is issued and no wait gives up any more)
+  if (threadIdx.x == 0 && bars->err) drain<C>(bars, S, &tmap_w, smem + (SWAP ? 0 : kRows * kBlockK));
 }
 
 constexpr int kSmemMax = 232448;   // dynamic shared memory of a CTA that has the SM to itself

@@ -13,6 +13,7 @@
 // activation quantizer's 16) that are consecutive across lanes, so a block of 128
 // columns is 16 (8) neighbouring lanes and its maximum takes four (three)
 // shuffles; K is a multiple of 16, so no lane straddles the end of a row.
+#include "fp8_drain.h"
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -28,6 +29,7 @@ namespace {
 constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126
 constexpr int kNormSlots = 8;                 // most row slots of a CTA
 constexpr int kNormSmem = 232448;             // shared memory of an SM for them
+constexpr uint64_t kNormWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -190,11 +192,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
   __shared__ uint64_t full[kNormSlots];
   __shared__ float red[2][32];
   __shared__ volatile int err;
+  __shared__ int left_out;  // rows not fetched since a wait gave up (thread 0's)
   const int t = threadIdx.x, threads = blockDim.x;
   const uint32_t row_bytes = (uint32_t)a.K * 2, slot_bytes = a.res ? 2 * row_bytes : row_bytes;
   if (t == 0) {
     for (int i = 0; i < slots; ++i) ptx::mbar_init(&full[i], 1);
     err = 0;
+    left_out = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -219,8 +223,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
   }
   int slot = 0, ph = 0, odd = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    // (after a wait that gave up, the CTA goes through its rows without waiting)
-    if (!err && !ptx::mbar_wait(&full[slot], ph, 2000000000ull)) {
+    // (after a wait that gave up, the CTA goes through its rows without waiting or
+    // fetching, so that all its threads meet at the same barriers)
+    bool landed = !err;
+    if (landed && !ptx::mbar_wait(&full[slot], ph, kNormWaitNs)) {
+      landed = false;
       err = 1;
       if (t == 0) atomicAdd(&g_fp8_norm_timeouts, 1u);
     }
@@ -251,8 +258,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
     __syncthreads();  // (the next row uses the other half of red)
     const int64_t next = row + (int64_t)slots * gridDim.x;
     if (t == 0 && next < a.M) {  // every thread has read its part of the slot
-      ptx::fence_proxy_async_smem();
-      fetch(next, slot);
+      if (landed) {
+        ptx::fence_proxy_async_smem();
+        fetch(next, slot);
+      } else {
+        ++left_out;
+      }
     }
     sum = warp_sum((t & 31) < (threads >> 5) ? red[odd][t & 31] : 0.0f);
     const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)a.K), a.eps));
@@ -290,6 +301,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
     }
     odd ^= 1;
     if (++slot == slots) slot = 0, ph ^= 1;
+  }
+  if (t == 0 && err) {
+    const int rows = (int)((a.M - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    drain_ring(rows - left_out, slots, [&](int i, int parity) { ptx::mbar_wait(&full[i], parity, kNormWaitNs); });
   }
 }
 
