@@ -43,7 +43,7 @@
 
 namespace nvfp4 {
 
-// CTAs whose pipeline wait ran past its limit, and group ends out of order or range.
+// CTAs whose pipeline wait ran past its limit, and calls with group ends out of order or range.
 __device__ unsigned int g_fp8_wait_timeouts = 0;
 __device__ unsigned int g_fp8_bad_offsets = 0;
 
@@ -469,8 +469,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
       }
-      if (lane == 0) pre[0] = 0;
-      if (bad && blockIdx.x == 0) atomicAdd(&g_fp8_bad_offsets, 1u);
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (lane == 0) {
+        pre[0] = 0;
+        if (bad && blockIdx.x == 0) atomicAdd(&g_fp8_bad_offsets, 1u);
+      }
     }
   }
   ptx::tc_fence_before();

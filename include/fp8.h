@@ -89,11 +89,13 @@ NVFP4_API nvfp4_status fp8_gemm(const uint8_t* x, const float* sx, const uint8_t
  * sw [E, ceil(N / 128), kb].  offsets: device int32 [E + 1], not decreasing,
  * within 0 .. T (e.g. written by a router earlier on the stream); experts may
  * have no rows.  Rows of Y outside offsets[0] .. offsets[E] - 1 keep what they
- * hold.  Offsets that decrease or leave 0 .. T are clamped (no row is read or
- * written outside X and Y) and counted for nvfp4_check_device_errors
- * (NVFP4_ERR_INVALID_ARG).  flags: NVFP4_FLAG_STATIC_WEIGHTS (changes nothing
- * here: the experts are known only after the preceding work).  1 <= E <=
- * FP8_MAX_EXPERTS, E * N < 2^31.  T == 0 or N == 0 is a no-op.
+ * hold.  Offsets that decrease or leave 0 .. T are clamped (each to 0 .. T, and
+ * an expert starts no earlier than any before it ends, so no row is read or
+ * written outside X and Y, and none twice); the call is counted for
+ * nvfp4_check_device_errors (NVFP4_ERR_INVALID_ARG).  flags:
+ * NVFP4_FLAG_STATIC_WEIGHTS (changes nothing here: the experts are known only
+ * after the preceding work).  1 <= E <= FP8_MAX_EXPERTS, E * N < 2^31.
+ * T == 0 or N == 0 is a no-op.
  */
 NVFP4_API nvfp4_status fp8_gemm_grouped(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                                         const int32_t* offsets, uint16_t* Y, int64_t ldy, int64_t T, int64_t E,
