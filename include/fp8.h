@@ -39,7 +39,8 @@ extern "C" {
 #endif
 
 /* fp8_quantize: X is [M, 2K], gate columns then up columns, and silu(gate) * up
- * is quantized (computed in fp32). */
+ * is quantized, computed in fp32 with silu within 2^-15 of itself (for silu a
+ * normal fp32 number, gates above -91). */
 #define FP8_FLAG_GATED 2u
 
 /* Most experts of one fp8_gemm_grouped call. */
