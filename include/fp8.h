@@ -76,7 +76,11 @@ NVFP4_API nvfp4_status fp8_quantize_weights(const uint16_t* W, int64_t ldw, int6
 
 /*
  * Y[m, n] = bf16_rne( sum_b sx[m, b] sw[n / 128, b] sum_{k in block b} x[m, k] w[n, k] ),
- * each block's sum on the tensor cores, the sum over blocks in fp32.
+ * each block's sum on the tensor cores (fp32), the sum over blocks in fp32.
+ * A block's sx * sw is formed first, in fp32, and should be a normal number there:
+ * below 2^-126 it has fewer bits (its share of the sum is off by up to 2^-150
+ * times the block's sum), from 2^128 on it is infinite and the output infinite or
+ * NaN, also where the block's sum is zero.
  * x, sx: activations [M, K]; w, sw: weights [N, K]; Y: BF16 [M, N], leading
  * dimension ldy.  Deterministic.  flags: NVFP4_FLAG_STATIC_WEIGHTS (w; sw is
  * read after the preceding work either way).  M == 0 or N == 0 is a no-op.
