@@ -14,6 +14,7 @@
 // columns is 16 (8) neighbouring lanes and its maximum takes four (three)
 // shuffles; K is a multiple of 16, so no lane straddles the end of a row.
 #include "fp8_drain.h"
+#include "fp8_plan.h"
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -27,8 +28,6 @@ __device__ unsigned int g_fp8_norm_timeouts = 0;
 namespace {
 
 constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126
-constexpr int kNormSlots = 8;                 // most row slots of a CTA
-constexpr int kNormSmem = 232448;             // shared memory of an SM for them
 constexpr uint64_t kNormWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int thr
 template <int VPT>
 __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, int slots) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint64_t full[kNormSlots];
+  __shared__ uint64_t full[plan::kNormSlots];
   __shared__ float red[2][32];
   __shared__ volatile int err;
   __shared__ int left_out;  // rows not fetched since a wait gave up (thread 0's)
@@ -466,6 +465,13 @@ __global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(const uint16_t*
   }
 }
 
+// Warps of a kernel that an SM's 65536 registers hold (a thread has them in eights).
+int warps_held(const void* fn) {
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, fn) != cudaSuccess) return 32;  // 64 a thread, the launch bound's most
+  return 65536 / 32 / ((attr.numRegs + 7) / 8 * 8);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* weight, const uint16_t* residual,
@@ -484,26 +490,19 @@ cudaError_t launch_fp8_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* w
     threads = (int)(((vecs + vpt - 1) / vpt + 31) / 32 * 32);
   }
   if (threads > 32 && M > 2 * (int64_t)sms) {
-    // about 20 warps per SM with a residual and 30 without (fewer bytes, more
-    // arithmetic per byte; measured from 2 to 6 CTAs at K = 1040 to 16384), and at
-    // least two CTAs with at least two rows each where the SM holds them
-    const int wide = vecs <= 2048 ? 2 : 4, group = (int)((vecs + wide - 1) / wide + 31) / 32 * 32;
-    const int slot = (int)K * (residual ? 4 : 2);
-    int per_sm = (residual ? 20 : 30) * 32 / group, slots = 0;
-    if (per_sm < 2 && 2 * group <= 2048) per_sm = 2;
-    for (; per_sm > 0; --per_sm) {
-      slots = (kNormSmem / per_sm - 2048) / slot;
-      if (slots >= 2) break;
-    }
-    if (slots > kNormSlots) slots = kNormSlots;
-    if (per_sm > 0) {
+    static const int warps[2] = {warps_held((const void*)rmsnorm_rows_kernel<2>),
+                                 warps_held((const void*)rmsnorm_rows_kernel<4>)};
+    const plan::NormRows p = plan::norm_rows(K, residual != nullptr, warps);
+    if (p.per_sm > 0) {
       static tc::SmemOptIn opt[2];
-      const void* fn = wide == 2 ? (const void*)rmsnorm_rows_kernel<2> : (const void*)rmsnorm_rows_kernel<4>;
-      cudaError_t e = opt[wide == 4].ensure(fn, slots * slot);
+      const void* fn = p.wide == 2 ? (const void*)rmsnorm_rows_kernel<2> : (const void*)rmsnorm_rows_kernel<4>;
+      const int smem = p.slots * (int)K * (residual ? 4 : 2);
+      cudaError_t e = opt[p.wide == 4].ensure(fn, smem);
       if (e != cudaSuccess) return e;
-      const int64_t grid = (int64_t)sms * per_sm;
+      const int64_t grid = (int64_t)sms * p.per_sm;
+      int slots = p.slots;
       void* args[] = {&a, &slots};
-      return tc::launch_pdl(fn, dim3((unsigned)(M < grid ? M : grid)), dim3(group), slots * slot, stream, args);
+      return tc::launch_pdl(fn, dim3((unsigned)(M < grid ? M : grid)), dim3(p.threads), smem, stream, args);
     }
   }
   const int rows = threads == 32 ? 4 : 1;
