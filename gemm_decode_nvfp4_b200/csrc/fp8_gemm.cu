@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 
 #include "fp8_drain.h"
+#include "fp8_plan.h"
 #include "nvfp4_device.cuh"
 #include "nvfp4_kernels.h"
 #include "sm100_ptx.cuh"
@@ -49,13 +50,13 @@ __device__ unsigned int g_fp8_bad_offsets = 0;
 
 namespace {
 
+using plan::Bars;
+using plan::kBlockK;
+using plan::kRows;
+using plan::kScaleSlots;
+
 constexpr long long kWaitClocks = 4000000000ll;  // about 2 s
 constexpr uint64_t kDrainNs = 2000000000ull;
-constexpr int kRows = 128;        // MMA M
-constexpr int kBlockK = 128;      // k per stage, one scale block, one swizzled row
-constexpr int kMaxStages = 8;
-constexpr int kMaxBufs = 4;
-constexpr int kScaleSlots = 16;
 constexpr int kGroupTiles = 16;   // token tiles that share a weight tile in the tile order
 
 struct Args {
@@ -68,43 +69,11 @@ struct Args {
   int stages, splits, static_weights;
 };
 
-struct Bars {
-  uint64_t full[kMaxStages];
-  uint64_t empty[kMaxStages];
-  uint64_t sfull[kScaleSlots];   // SWAP: a block's scales are in its slot
-  uint64_t sempty[kScaleSlots];  //       its block has been promoted
-  uint64_t acc_full[kMaxBufs];
-  uint64_t acc_empty[kMaxBufs];
-  uint64_t mma_done;
-  uint32_t tmem_addr;
-  volatile int err;
-  int issued[2];  // loads of the tokens' and the weights' tiles, when their producers are done
-};
-
 // !SWAP: 168 registers a thread (384 threads) do not hold 128 accumulators and
 // the loads in flight, and a spill costs a trip to L2 (shared memory leaves no
 // L1), so the promotion warps take over registers of the other warpgroup:
 // 256 x 224 + 128 x 56 = 384 x 168.
 constexpr int kRegsMore = 224, kRegsLess = 56;
-
-template <bool SWAP_, int BN_, int PW_>
-struct Cfg {
-  static constexpr bool SWAP = SWAP_;
-  static constexpr int BN = BN_, PW = PW_;
-  static constexpr int NBUF = 512 / BN < kMaxBufs ? 512 / BN : kMaxBufs;
-  static constexpr uint32_t TMEM = NBUF * BN < 32 ? 32 : NBUF * BN;
-  static constexpr int COLS = BN / (PW / 4);  // accumulator columns of one thread
-  static constexpr int TOK = SWAP ? BN : kRows, WROWS = SWAP ? kRows : BN;
-  static constexpr int LD = SWAP ? 16 : 32;  // columns of a tensor-memory load (of 16 at a time) ...
-  static constexpr int LDBUF = 2;            // ... and the register buffers for them
-  static constexpr int SLOT = TOK + 4;       // floats of a scale slot: token scales, then the weight scale
-  static constexpr int STAGE = (kRows + BN) * kBlockK;
-  static constexpr int THREADS = (PW + 4) * 32;
-  static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
-  static constexpr int EPI = SWAP ? 0 : PW * 2176;
-  static constexpr int SCALES = SWAP ? kScaleSlots * SLOT * 4 : 0;
-  static constexpr int FIXED = EPI + SCALES + (int)sizeof(Bars) + 1024;
-};
 
 // Wait for the phase with the given parity, kWaitClocks at most; then the CTA's
 // error is recorded and its other waits fail too.
@@ -733,102 +702,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   if (threadIdx.x == 0 && bars->err) drain<C>(bars, S, &tmap_w, smem + (SWAP ? 0 : kRows * kBlockK));
 }
 
-constexpr int kSmemMax = 232448;   // dynamic shared memory of a CTA that has the SM to itself
-constexpr int kSmemHalf = 115712;  // of one that shares it with another
-
-int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
-
-template <class C>
-int stages_of(int table) {
-  const int n = ((C::CTAS == 2 ? kSmemHalf : kSmemMax) - C::FIXED - table) / C::STAGE;
-  return n < kMaxStages ? n : kMaxStages;
-}
-
-// CTAs of clusters of c that run at once.  A cluster stays within one GPC, so a
-// few SMs are left over; in thousandths of the SMs, as the occupancy of an empty
-// kernel with this shared memory has it on one B200 (148 SMs).  (Of this kernel
-// the driver reports one CTA per SM whatever its size, but two do run.)
-template <class C>
-int64_t resident(int c, int sms) {
-  constexpr int one[9] = {0, 1000, 1000, 912, 891, 878, 891, 709, 810};
-  constexpr int two[9] = {0, 1000, 1000, 942, 959, 945, 912, 875, 891};
-  return (int64_t)sms * C::CTAS * (C::CTAS == 2 ? two[c] : one[c]) / 1000;
-}
-
-struct Problem {
+struct Launch {
   const uint8_t* x;
   const uint8_t* w;
   Args a;
-  int64_t active;  // experts that may have rows, 0: dense
-  int sms;
+  plan::Product p;
   cudaStream_t stream;
-
-  // Token tiles of `tok` rows: of a grouped call an estimate (half a tile per
-  // expert is empty), or the most there can be.
-  template <class C>
-  int64_t tiles(bool most) const {
-    const int64_t mt = a.offsets ? a.T / C::TOK + (most ? a.E : (active + 1) / 2) : cdiv(a.T, C::TOK);
-    return mt * cdiv(a.N, C::WROWS);
-  }
-
-  // Estimated microseconds of a configuration with c CTAs sharing each tile's k:
-  // waves of CTAs times blocks of k, and the time to read the weights
-  // (6.3 TB/s, which nine tenths of the SMs reach); the longer one counts in full,
-  // the other one, mostly behind it, a quarter.
-  // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
-  // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
-  // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
-  // 0.8 and 0.025 per token of the tile.  The choices by this rule run within 7%
-  // of the best one of each shape there but for one (19%); by tile width alone
-  // (M <= 16: 16 tokens, and so on) they were up to 2.7 times slower.
-  template <class C>
-  double estimate(int c) const {
-    constexpr double alone = C::BN == 16 ? 0.19 : C::BN == 32 ? 0.24 : C::BN == 64 ? 0.40 : C::BN == 128 ? 0.38 : 0.40;
-    constexpr double full = C::BN == 16 ? 0.29 : C::BN == 32 ? 0.36 : C::BN == 64 ? 0.52 : C::BN == 128 ? 0.45 : 0.51;
-    constexpr double store = C::BN == 16 ? 0.5 : C::BN == 32 ? 0.7 : C::BN == 64 ? 1.0 : 1.5;
-    const int64_t slots = resident<C>(c, sms), ctas = tiles<C>(false) * c;
-    const double per_block = ctas > (C::BN >= 128 ? 100 : sms) ? full : alone;
-    const double work = (double)cdiv(ctas, slots) * ((double)cdiv(a.kb, c) * per_block + store);
-    const double bytes = (double)(active ? active : 1) * a.N * a.K + (double)a.T * (a.K + 2.0 * a.N);
-    const double stream = bytes / 6.3e6 * (ctas < 0.92 * sms ? 0.92 * sms / ctas : 1.0);
-    return (work > stream ? work + 0.25 * stream : stream + 0.25 * work) + (c > 1 ? 0.8 + 0.025 * C::BN : 0.0);
-  }
-
-  template <class C>
-  void consider(double& best, int& bn, int& splits) const {
-    if (stages_of<C>(a.offsets ? 3 * (a.E + 1) * 4 : 0) < 2) return;
-    // (a grouped call's tiles are not known here, so a cluster per tile cannot be)
-    const int most = C::SWAP && !a.offsets ? (a.kb < 8 ? a.kb : 8) : 1;
-    for (int c = 1; c <= most; ++c) {
-      if (c > 1 && tiles<C>(true) * c > 4 * (int64_t)sms) break;  // enough tiles to fill the GPU
-      const double t = estimate<C>(c);
-      if (t < best) {
-        best = t;
-        bn = C::BN;
-        splits = c;
-      }
-    }
-  }
 
   template <class C>
   cudaError_t run(int splits) const {
     static tc::SmemOptIn opt;
     Args b = a;
     b.splits = splits;
-    b.nt = (int)cdiv(a.N, C::WROWS);
-    const int table = a.offsets ? 3 * (a.E + 1) * 4 : 0;
-    b.stages = stages_of<C>(table);
+    b.nt = (int)plan::cdiv(a.N, C::WROWS);
+    b.stages = plan::stages_of<C>(p.table());
     CUtensorMap mw, mx;
     if (!tc::make_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)a.K, (uint64_t)a.E * a.N, (uint64_t)a.K,
                           kBlockK, C::WROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tc::make_tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)a.K, (uint64_t)a.T, (uint64_t)a.K, kBlockK,
                           C::TOK, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
-    const int smem = C::FIXED + table + b.stages * C::STAGE;
+    const int smem = C::FIXED + p.table() + b.stages * C::STAGE;
     const void* fn = (const void*)fp8_gemm_kernel<C>;
     cudaError_t e = opt.ensure(fn, smem);
     if (e != cudaSuccess) return e;
-    const int64_t n = tiles<C>(true), slots = (int64_t)sms * C::CTAS;
+    const int64_t n = p.tiles<C>(true), slots = (int64_t)p.sms * C::CTAS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(splits > 1 ? n * splits : n < slots ? n : slots));
     cfg.blockDim = dim3(C::THREADS);
@@ -846,12 +744,6 @@ struct Problem {
   }
 };
 
-using S16 = Cfg<true, 16, 4>;
-using S32 = Cfg<true, 32, 4>;
-using S64 = Cfg<true, 64, 8>;
-using S128 = Cfg<true, 128, 16>;
-using L256 = Cfg<false, 256, 8>;
-
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, const int* offsets,
@@ -867,22 +759,16 @@ cudaError_t launch_fp8_gemm(const uint8_t* x, const float* sx, const uint8_t* w,
   a.N = (int)N;
   a.K = (int)K;
   a.E = (int)E;
-  a.kb = (int)cdiv(K, kBlockK);
+  a.kb = (int)plan::cdiv(K, kBlockK);
   a.static_weights = static_weights;
-  const Problem p{x, w, a, offsets ? (E < T ? E : T) : 0, sms, stream};
-  double best = 1e300;
-  int bn = 0, splits = 1;
-  p.consider<S16>(best, bn, splits);
-  p.consider<S32>(best, bn, splits);
-  p.consider<S64>(best, bn, splits);
-  p.consider<S128>(best, bn, splits);
-  p.consider<L256>(best, bn, splits);
-  switch (bn) {
-    case 16: return p.run<S16>(splits);
-    case 32: return p.run<S32>(splits);
-    case 64: return p.run<S64>(splits);
-    case 128: return p.run<S128>(splits);
-    case 256: return p.run<L256>(splits);
+  const Launch l{x, w, a, plan::Product(T, E, N, K, offsets != nullptr, sms), stream};
+  const plan::Choice c = l.p.choose();
+  switch (c.bn) {
+    case 16: return l.run<plan::S16>(c.splits);
+    case 32: return l.run<plan::S32>(c.splits);
+    case 64: return l.run<plan::S64>(c.splits);
+    case 128: return l.run<plan::S128>(c.splits);
+    case 256: return l.run<plan::L256>(c.splits);
   }
   return cudaErrorInvalidConfiguration;
 }

@@ -51,3 +51,40 @@ def test_two_norm_ctas_where_the_registers_hold_them(plan):
     assert norm_rows(plan, 9216, False, (64, 64))[1:3] == (576, 1)
     assert norm_rows(plan, 5120, False, (55, 64))[2:] == (3, 7)
     assert norm_rows(plan, 5120, True, (55, 64))[2:] == (2, 5)
+
+
+SMS = 148
+WIDTHS = (16, 32, 64, 128, 256)
+
+
+def choice(plan, T, E, N, K, grouped):
+    out = (ctypes.c_int * 2)()
+    plan.gemm_choice(*(ctypes.c_int64(v) for v in (T, E, N, K)), int(grouped), SMS, out)
+    return tuple(out)
+
+
+def test_gpu_tests_reach_every_configuration_of_the_products(plan):
+    """Each size of test_gpu_fp8_choices takes the configuration that it is listed under,
+    and over 200000 random shapes no other configuration is chosen."""
+    from test_gpu_fp8_choices import DENSE, GROUPED
+    assert {s: choice(plan, s[0], 1, s[1], s[2], False) for s in DENSE.values()} == \
+        {shape: pair for pair, shape in DENSE.items()}
+    assert {w: choice(plan, *s, True) for w, s in GROUPED.items()} == {w: (w, 1) for w in WIDTHS}
+    counts, shapes = (ctypes.c_int * 40)(), (ctypes.c_int64 * 120)()
+    plan.scan_choices(200000, ctypes.c_uint64(3), SMS, counts, shapes)
+    found = {(w, c + 1): tuple(shapes[3 * (8 * i + c):][:3]) for i, w in enumerate(WIDTHS) for c in range(8)
+             if counts[8 * i + c]}
+    assert not set(found) - set(DENSE), {k: v for k, v in found.items() if k not in DENSE}
+
+
+def test_a_split_has_a_block_for_every_cta(plan):
+    for K in range(16, 1100, 16):
+        for M, N in ((1, 64), (33, 640), (120, 5120)):
+            assert choice(plan, M, 1, N, K, False)[1] <= -(-K // 128)
+
+
+def test_grouped_products_are_not_split(plan):
+    for T in (1, 7, 64, 1000, 30000):
+        for E in (1, 8, 160, 4096):
+            width, splits = choice(plan, T, E, 1536, 2048, True)
+            assert width in WIDTHS and splits == 1
