@@ -195,12 +195,12 @@ struct ScaleStream {
   bool vec;
   __device__ __forceinline__ void fetch(int kb, int kbs) {
     if (vec) {  // rows of whole 16-byte groups
-      nx = __ldg(reinterpret_cast<const float4*>(x + kb));
-      nw = __ldg(reinterpret_cast<const float4*>(w + kb));
+      nx = *reinterpret_cast<const float4*>(x + kb);
+      nw = *reinterpret_cast<const float4*>(w + kb);
     } else {
       const int b = min(kb + 1, kbs - 1), c = min(kb + 2, kbs - 1), d = min(kb + 3, kbs - 1);
-      nx = make_float4(__ldg(x + kb), __ldg(x + b), __ldg(x + c), __ldg(x + d));
-      nw = make_float4(__ldg(w + kb), __ldg(w + b), __ldg(w + c), __ldg(w + d));
+      nx = make_float4(x[kb], x[b], x[c], x[d]);
+      nw = make_float4(w[kb], w[b], w[c], w[d]);
     }
   }
   __device__ __forceinline__ void start(const float* x_, const float* w_, int kbs, bool vec_) {

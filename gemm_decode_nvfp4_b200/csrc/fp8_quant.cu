@@ -30,6 +30,19 @@ namespace {
 constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126
 constexpr uint64_t kNormWaitNs = 2000000000ull;
 
+// 16-byte load of what is read once, past L1.  Not a read-only load (ld.global.nc,
+// __ldg): those are for data that nothing writes while the kernel runs, and these
+// kernels' CTAs start while the kernels before them may still be writing what they
+// read after their wait.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int thr
     const int c = (t + i * threads) * 8;
     if (c < a.K) {
       load_h(a, row, c, f[i]);
-      wv[i] = __ldg(reinterpret_cast<const uint4*>(a.w + c));
+      wv[i] = *reinterpret_cast<const uint4*>(a.w + c);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, in
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (t * VPT + i) * 8;
-    wv[i] = c < a.K ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
+    wv[i] = c < a.K ? *reinterpret_cast<const uint4*>(a.w + c) : make_uint4(0, 0, 0, 0);
   }
   int slot = 0, ph = 0, odd = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
     uint4 wv = make_uint4(0, 0, 0, 0);
     if (in) {
       load_h(b, row, c, f);
-      wv = __ldg(reinterpret_cast<const uint4*>(a.w + c));
+      wv = *reinterpret_cast<const uint4*>(a.w + c);
     }
     norm_out(a, row, c, in, f, wv, rstd);
   }
@@ -393,11 +406,11 @@ __global__ void __launch_bounds__(256, 6) quantize_rows_kernel(const QuantArgs a
     float f[2][8] = {};
     if (in) {
       const uint16_t* p = a.x + (int64_t)row * a.ldx + c;
-      const uint4 v0 = ld_stream_v4(p), v1 = ld_stream_v4(p + 8);
+      const uint4 v0 = ld_once_v4(p), v1 = ld_once_v4(p + 8);
       unpack8(v0, f[0]);
       unpack8(v1, f[1]);
       if (GATED) {
-        const uint4 u0 = ld_stream_v4(p + a.K), u1 = ld_stream_v4(p + a.K + 8);
+        const uint4 u0 = ld_once_v4(p + a.K), u1 = ld_once_v4(p + a.K + 8);
         float uf[8];
         unpack8(u0, uf);
 #pragma unroll
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(256, 6) quantize_rows_kernel(const QuantArgs a
 
 // Weight quantizer: one CTA of 256 threads per 128 x 128 block, held in
 // registers between the maximum and the codes.
-__global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(const uint16_t* __restrict__ w, int64_t ldw, int64_t N,
+__global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(const uint16_t* w, int64_t ldw, int64_t N,
                                                               int K, int kb, uint8_t* __restrict__ q,
                                                               float* __restrict__ s) {
   __shared__ float red[8];
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(const uint16_t*
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t n = row0 + 16 * i;
-    v[i] = n < N && c < K ? ld_stream_v4(w + n * ldw + c) : make_uint4(0, 0, 0, 0);
+    v[i] = n < N && c < K ? ld_once_v4(w + n * ldw + c) : make_uint4(0, 0, 0, 0);
   }
   float m = 0.0f;
 #pragma unroll
