@@ -18,10 +18,11 @@
 //         many tokens.
 // Roles per CTA: PW promotion warps; two producer threads (TMA tiles of the tokens
 // and of the weights); one MMA warp; SWAP: a warp that copies the block's scales
-// into a ring of slots with cp.async.  Persistent over tiles; the stage ring runs
-// on across tiles.  With few tiles a cluster of `splits` CTAs shares a tile's
-// blocks of k and adds the partial sums in rank order through distributed shared
-// memory.  Every wait is bounded.
+// into a ring of slots with cp.async (!SWAP: a warp without a role, part of the
+// warpgroup whose registers setmaxnreg moves).  Persistent over tiles; the stage
+// ring runs on across tiles.  With few tiles a cluster of `splits` CTAs shares a
+// tile's blocks of k and adds the partial sums in rank order through distributed
+// shared memory.  Every wait is bounded.
 //
 // What bounds it (one B200): few tokens, the weight stream (one token through
 // 17408 x 5120: 17.0 us, 81% of the copy rate); many, the power limit (4096 tokens
@@ -605,14 +606,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             ptx::tc_fence_before();
             if (elect_one()) ptx::mbar_arrive(&bars->acc_empty[buf]);
           }
-          if (NR > 1 && c + 1 < NLD) tmem_ld(lane_addr + buf * BN + LD * (c + 1), r[(c + 1) % NR]);
+          if (c + 1 < NLD) tmem_ld(lane_addr + buf * BN + LD * (c + 1), r[(c + 1) % NR]);
 #pragma unroll
           for (int j = 0; j < LD / 2; ++j) {
             const uint64_t s =
                 SWAP ? mul2(*reinterpret_cast<const uint64_t*>(sc + col0 + LD * c + 2 * j), sw2) : srow;
             fma2(acc[LD / 2 * c + j], r[c % NR][2 * j], r[c % NR][2 * j + 1], s);
           }
-          if (NR == 1 && c + 1 < NLD) tmem_ld(lane_addr + buf * BN + LD * (c + 1), r[0]);
         }
         if (++buf == NBUF) buf = 0, bph ^= 1;
         if constexpr (SWAP) {
