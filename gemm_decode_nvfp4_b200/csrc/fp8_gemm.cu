@@ -25,13 +25,14 @@
 // shared memory.  Every wait is bounded.
 //
 // What bounds it (one B200): few tokens, the weight stream (one token through
-// 17408 x 5120: 17.0 us, 81% of the copy rate); many, the power limit (4096 tokens
-// through 17408 x 5120: 298 us or 2.45 PFLOP/s in a burst, 362 us at 1.5 GHz in a
-// loop) and L2 to SM: bulk copies alone reach 58 bytes per cycle and SM, so a
+// 17408 x 5120: 17.1 us, 81% of the copy rate); many, the power limit (4096 tokens
+// through 17408 x 5120: 350 to 370 us at 1.5 GHz in a loop, 298 us or 2.45 PFLOP/s in
+// a short burst) and L2 to SM: bulk copies alone reach 58 bytes per cycle and SM, so a
 // 128 x 256 x 128 block's 48 KB take 847 cycles against 512 of MMAs, and a block
 // takes 850 to 880.  Pairs of SMs with 256 x 256 tiles, which load a third less,
-// ran at 330 us: the chain commit, promotion, arrival at the other SM, next MMA is
-// longer than two accumulators cover.
+// ran at 330 us in bursts: the chain commit, promotion, arrival at the other SM, next
+// MMA is longer than two accumulators cover.  Short K and middle batches: the stores
+// of a tile (1.5 us) and the sums of a split.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -56,7 +57,7 @@ using plan::kBlockK;
 using plan::kRows;
 using plan::kScaleSlots;
 
-constexpr long long kWaitClocks = 4000000000ll;  // about 2 s
+constexpr long long kWaitClocks = 4000000000ll;  // 2.0 s at 1.965 GHz, 2.7 s at 1.5 GHz
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kGroupTiles = 16;   // token tiles that share a weight tile in the tile order
 

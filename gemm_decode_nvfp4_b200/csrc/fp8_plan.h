@@ -144,9 +144,10 @@ struct Product {
   // Measured on one B200 (M 1 to 1024, N 1024 to 17408, K 2048 to 17408): a block
   // of k takes `alone` us with one CTA on an SM and `full` with all SMs (and both
   // CTAs of one) busy, a tile's epilogue `store`, adding the shares of a split
-  // 0.8 and 0.025 per token of the tile.  The choices by this rule run within 7%
-  // of the best one of each shape there but for one (19%); by tile width alone
-  // (M <= 16: 16 tokens, and so on) they were up to 2.7 times slower.
+  // 0.8 and 0.025 per token of the tile.  The choices by this rule ran within 7%
+  // of the best one of each of 59 shapes there but for one (19%); by tile width alone
+  // (M <= 16: 16 tokens, and so on) they were up to 2.7 times slower.  K below 2048
+  // and M above 1024 were not measured against the other configurations.
   template <class C>
   double estimate(int c) const {
     constexpr double alone = C::BN == 16 ? 0.19 : C::BN == 32 ? 0.24 : C::BN == 64 ? 0.40 : C::BN == 128 ? 0.38 : 0.40;

@@ -9,10 +9,11 @@
 // fmaxf drops NaN, so a NaN element stays a NaN code of its own and leaves the
 // rest of its block alone; an infinity makes its block's scale infinite.
 //
-// All three stream HBM once.  A thread owns 16-byte vectors (8 columns; the
-// activation quantizer's 16) that are consecutive across lanes, so a block of 128
-// columns is 16 (8) neighbouring lanes and its maximum takes four (three)
-// shuffles; K is a multiple of 16, so no lane straddles the end of a row.
+// All three stream HBM once (norm rows of more than 32768 columns twice).  A thread
+// owns 16-byte vectors of 8 columns, so a block of 128 columns is neighbouring lanes:
+// 8 of two vectors in the activation quantizer, 16 of one in the norm of few rows, 8 or
+// 4 of two or four in that of many; K is a multiple of 16, so no lane straddles the
+// end of a row.
 #include "fp8_drain.h"
 #include "fp8_plan.h"
 #include "nvfp4_device.cuh"
@@ -195,9 +196,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int thr
 // bring them into a ring of row slots (x, then the residual) ahead of time, so
 // that reads go on while a row is summed, scaled and stored.  A thread has VPT
 // neighbouring vectors, so a block of 128 columns is 16 / VPT lanes.  8192 rows of
-// 5120 with a residual (295 MB): 51.7 us, 88% of the copy rate; a CTA per row, its
+// 5120 with a residual (295 MB): 49.6 us, 92% of the copy rate; a CTA per row, its
 // loads waiting for its place on the SM, 73.6 us.  Without the residual the
-// arithmetic per byte bounds it (8192 x 5120: 38 us, 52%).
+// arithmetic per byte bounds it (8192 x 5120: 36.4 us, 54%).
 template <int VPT>
 __global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const NormArgs a, int slots) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -387,8 +388,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // Activation quantizer: 8 lanes of 16 columns per block of 128, two (gated: four)
-// 16-byte loads of a lane in flight at six CTAs per SM.  4096 x 5120: 12.4 us, 80%
-// of the copy rate; gated 1024 x 17408: 17.5 us, 80%.  (16 lanes of 8 columns at
+// 16-byte loads of a lane in flight at six CTAs per SM.  4096 x 5120: 12.1 us, 81%
+// of the copy rate; gated 1024 x 17408: 16.5 us, 84%.  (16 lanes of 8 columns at
 // eight CTAs: 14.6 and 20.2 us; two or four blocks of a lane in flight with as many
 // fewer warps: 14.9 to 18.9 us.)
 template <bool GATED>
