@@ -97,7 +97,8 @@ def _check(fn: str, status: int) -> None:
 
 
 def check_device_errors() -> None:
-    """Raise if a tensor-core GEMM CTA gave up on a bounded pipeline wait."""
+    """Raise if a CTA gave up on a bounded pipeline wait, or a grouped call had ids or
+    offsets out of range (nvfp4_check_device_errors)."""
     _check("nvfp4_check_device_errors", lib.nvfp4_check_device_errors())
 
 

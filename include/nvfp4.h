@@ -283,8 +283,8 @@ NVFP4_API nvfp4_status nvfp4_gemv_grouped(const uint16_t* X, int64_t ldx, const 
 /*
  * Diagnostic: every wait inside the pipelined kernels (the tensor-core GEMMs,
  * the W4A4 GEMM of nvfp4_w4a4.h, the norm and products of fp8.h and the TMA-fed
- * decode GEMV) is bounded
- * (about 2 s); a CTA that gives up records it in a device counter and finishes
+ * decode GEMV) is bounded (about 2 s, the fp8 products' up to 3 s at a low
+ * clock); a CTA that gives up records it in a device counter and finishes
  * without hanging, leaving its outputs undefined.  This call reads and clears
  * those counters for the current device (it waits for prior work on the
  * legacy default stream) and returns NVFP4_ERR_TIMEOUT if one was non-zero,
